@@ -35,6 +35,12 @@
  *                     lifted activations for (2N-2):2N. SlideSparse sec. 2C
  *                     item 3 (online phase).
  *   nm_dense_gemm     Y = X * W^T, dense tcgen05 GEMM (the comparison point).
+ *   nm_sparse_glu     H = act(X Wg^T) (.) (X Wu^T), a gated feed-forward's first
+ *                     half with both projections sparse, in one kernel.
+ *   nm_sparse_glu_backward  its gradients.
+ *   nm_sparse_gemm_lora  Y = X W_sparse^T + the low-rank adapters of many
+ *                     requests, in one product.
+ *   nm_sparse_densify mask (.) V in dense form from the kept values.
  *   nm_ternary_quantize  gamma = mean|W|, W_q = clip(rint(W/gamma),-1,1)*gamma.
  *                     Sparse-BitNet sec. 1 item 1 (BitNet b1.58 ternary weights).
  *
@@ -364,6 +370,97 @@ size_t nm_dense_gemm_workspace_bytes(int64_t T, int64_t K, int64_t R);
 nm_status nm_dense_gemm(const uint16_t *X, int64_t T, int64_t K, int64_t ldx, const uint16_t *W,
                         int64_t R, int64_t ldw, uint16_t *Y, int64_t ldy, void *ws,
                         size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------ */
+/* Gated feed-forward, first half, with both projections sparse:
+ *   G = X Wg^T, U = X Wu^T, H[t, r] = bf16(act(G[t, r]) * U[t, r])
+ * G and U are the fp32 sums in tensor memory; H is rounded once.  One kernel
+ * computes both products, the activation and the gate; neither G nor U is
+ * written unless asked for.
+ *   act : NM_ACT_SILU  g / (1 + e^-g);
+ *         NM_ACT_GELU  the tanh form, g (1 + tanh z) / 2 with z =
+ *                      sqrt(2/pi) (g + 0.044715 g^3);
+ *         NM_ACT_RELU2 max(g, 0)^2.   Others -> NM_ERR_UNSUPPORTED.
+ *   X   : [T x K] bf16, ldx >= K.   H : [T x R] bf16, ldh >= R.
+ *   packed_gate, packed_up: nm_sparse_prepare(..., R, K, m, ...) of Wg and Wu
+ *         (the same R, K and m; m in {4, 6, 8, 10}).  They may be one buffer.
+ *   G, U: [T x R] bf16 (row stride ldgu >= R), both or neither (NULL): rounded
+ *         from the same fp32 sums, for nm_sparse_glu_backward.
+ *   ws  : as for nm_sparse_gemm, with nm_sparse_glu_workspace_bytes(T, K, m):
+ *         too small for the staged activations -> NM_ERR_WORKSPACE; without
+ *         the rest (NULL for 2:4) whole tiles only.  Not to be shared by calls
+ *         that may run at the same time.  A captured call may be replayed, and
+ *         graphs that never run at the same time may share it.
+ * Any T >= 1.  Infinities and NaN of the sums pass through the formulas.     */
+enum { NM_ACT_SILU = 0, NM_ACT_GELU = 1, NM_ACT_RELU2 = 2 };
+size_t nm_sparse_glu_workspace_bytes(int64_t T, int64_t K, int m);
+nm_status nm_sparse_glu(const uint16_t *X, int64_t T, int64_t K, int64_t ldx, const void *packed_gate,
+                        const void *packed_up, int64_t R, int m, int act, uint16_t *H, int64_t ldh,
+                        uint16_t *G, uint16_t *U, int64_t ldgu, void *ws, size_t ws_bytes, void *stream);
+
+/* Gradients of nm_sparse_glu from dH [T x R] and the G, U that it kept:
+ *   dG = dH U act'(G), dU = dH act(G)   (fp32, each rounded once to bf16, the
+ *                                        type of the tensor cores' operands)
+ *   dX = dG Wg + dU Wu                  [T x K] bf16
+ *   dWg = dG^T X, dWu = dU^T X          [R x K] bf16, fp32 accumulation
+ *   Wg, Wu : the masked weights in dense form [R x K] bf16 (nm_sparse_densify;
+ *            row stride ldw >= K).  The transpose of an (m-2):m matrix is not
+ *            (m-2):m, so dX runs on the dense tensor cores.
+ *   mask_gate, mask_up : both NULL: dWg and dWu are the gradients of every
+ *            weight (straight through the mask, to the latent weights); or
+ *            the masks of nm_prune_compress (pattern width m, 2 <= m <= 16): the
+ *            gradients of the kept weights, zero elsewhere.
+ *   dX, or dWg and dWu, may be NULL: then not computed (dX NULL: Wg, Wu unused;
+ *            dWg NULL: X unused).
+ *   ws  : nm_sparse_glu_backward_workspace_bytes(T, R) bytes, 16-byte aligned
+ *         (dG and dU).  Not to be shared by calls that may run at the same time.
+ * Sums run in a fixed order: repeated calls agree bit for bit.               */
+size_t nm_sparse_glu_backward_workspace_bytes(int64_t T, int64_t R);
+nm_status nm_sparse_glu_backward(const uint16_t *dH, int64_t lddh, const uint16_t *X, int64_t T, int64_t K,
+                                 int64_t ldx, const uint16_t *G, const uint16_t *U, int64_t ldgu,
+                                 const uint16_t *Wg, const uint16_t *Wu, int64_t R, int64_t ldw, int act,
+                                 const uint32_t *mask_gate, const uint32_t *mask_up, int m, uint16_t *dX,
+                                 int64_t lddx, uint16_t *dWg, uint16_t *dWu, int64_t lddw, void *ws,
+                                 size_t ws_bytes, void *stream);
+
+/* W = mask (.) V in dense form, from nm_prune_compress's kept values and mask
+ * (1 <= n < m <= 16): W [R x K] bf16, ldw >= K, ldw % 8 == 0, 16-byte aligned.
+ * What nm_dense_gemm and nm_sparse_glu_backward take.  A group that does not
+ * hold exactly n kept positions sets NM_ERR_DEVICE in the device error word. */
+nm_status nm_sparse_densify(const uint16_t *vals, const uint32_t *mask, int64_t R, int64_t K, int n, int m,
+                            uint16_t *W, int64_t ldw, void *stream);
+
+/* A sparse projection with the low-rank adapters of many requests at once:
+ *   Y[t, r] = sum_k X[t,k] W[r,k] + scale[a] sum_j V[t,j] B[a][r,j],
+ *   V[t, j] = sum_k X[t,k] A[a][j,k],   a = the adapter of t's request.
+ * W as in nm_sparse_gemm.  scale * V is rounded once to bf16 (a tensor-core
+ * operand); its product joins the projection's fp32 sum, Y is rounded once.
+ *   A : `adapters` matrices [r x K] bf16, row stride lda >= K, matrix stride
+ *       sda.   B : `adapters` matrices [R x r] bf16, ldb >= r, sdb.
+ *       All strides multiples of 8.  r a multiple of 8, 8 <= r <=
+ *       NM_LORA_MAX_RANK (else NM_ERR_UNSUPPORTED); adapters of lower rank are
+ *       padded with zero rows of A.   scale : [adapters] fp32.
+ *   indptr : int32 [requests + 1], ids : int32 [requests], on the device.
+ *       Request i has the tokens [indptr[i], indptr[i+1]), possibly none, and
+ *       adapter ids[i], or none where ids[i] is -1.  Requests may share
+ *       adapters.  Tokens before the first request or behind the last one get
+ *       the projection alone.  requests may be 0.
+ *       A list that is not ascending within [0, T], or an id outside [-1,
+ *       adapters), sets NM_ERR_DEVICE in the device error word; the outputs are
+ *       then unspecified, and no memory outside the arguments is touched.
+ *   ws : nm_sparse_gemm_lora_workspace_bytes(...) bytes, 16-byte aligned,
+ *       required.  Not to be shared by calls that may run at the same time.  A
+ *       captured call may be replayed (with other contents of every array), and
+ *       graphs that never run at the same time may share it.               */
+#define NM_LORA_MAX_RANK 256
+size_t nm_sparse_gemm_lora_workspace_bytes(int64_t T, int64_t K, int m, int64_t r, int64_t adapters,
+                                           int64_t requests);
+nm_status nm_sparse_gemm_lora(const uint16_t *X, int64_t T, int64_t K, int64_t ldx, const void *packed,
+                              int64_t R, int m, const uint16_t *A, int64_t lda, int64_t sda,
+                              const uint16_t *B, int64_t ldb, int64_t sdb, const float *scale,
+                              int64_t adapters, int64_t r, const int32_t *indptr, const int32_t *ids,
+                              int64_t requests, uint16_t *Y, int64_t ldy, void *ws, size_t ws_bytes,
+                              void *stream);
 
 /* Upper bound on the CTA pairs a stream-K launch uses (its partial-sum
  * region is sized for this many: 2*8 slots of 32 x 240 fp32 plus 2*8 64-bit

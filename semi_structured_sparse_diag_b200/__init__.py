@@ -10,6 +10,7 @@ bf16 tensors may be given as ``torch.bfloat16`` or as ``torch.uint16`` /
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -22,7 +23,7 @@ __all__ = [
     "NMError", "load", "hessian_diag", "score", "score_from_hessian", "prune_compress",
     "score_prune_compress", "hessian_rescale", "hutchinson_diag", "quant_lift_f8", "sparse_prepare_f8",
     "sparse_gemm_f8", "slide_pack", "lift_activations", "sparse_prepare", "sparse_prepare_from_mask",
-    "sparse_gemm", "dense_gemm",
+    "sparse_gemm", "dense_gemm", "sparse_glu", "sparse_glu_backward", "sparse_gemm_lora", "sparse_densify",
     "ternary_quantize", "check_device_error", "set_gemm_schedule", "set_poison", "EXPORTED",
 ]
 
@@ -37,6 +38,8 @@ EXPORTED = (
     "nm_hutchinson_workspace_bytes", "nm_hutchinson_diag", "nm_lifted_cols_f8", "nm_sparse_prepare_f8_bytes",
     "nm_quant_lift_f8", "nm_sparse_prepare_f8", "nm_sparse_gemm_f8", "nm_test_set_wait_limit_ns",
     "nm_test_withhold_stream_k_flag", "nm_test_hessian_clusters", "nm_hessian_launch_count", "nm_sparse_prepare_from_mask",
+    "nm_sparse_glu_workspace_bytes", "nm_sparse_glu", "nm_sparse_glu_backward_workspace_bytes",
+    "nm_sparse_glu_backward", "nm_sparse_densify", "nm_sparse_gemm_lora_workspace_bytes", "nm_sparse_gemm_lora",
 )
 
 _P, _I64, _I, _D, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_double, ctypes.c_size_t
@@ -80,6 +83,15 @@ _SIGS = {
     "nm_test_withhold_stream_k_flag": (_I, [_I]),
     "nm_test_hessian_clusters": (_I, [_I]),
     "nm_hessian_launch_count": (_I, [_I64, _I64]),
+    "nm_sparse_glu_workspace_bytes": (_SZ, [_I64, _I64, _I]),
+    "nm_sparse_glu": (_I, [_P, _I64, _I64, _I64, _P, _P, _I64, _I, _I, _P, _I64, _P, _P, _I64, _P, _SZ, _P]),
+    "nm_sparse_glu_backward_workspace_bytes": (_SZ, [_I64, _I64]),
+    "nm_sparse_glu_backward": (_I, [_P, _I64, _P, _I64, _I64, _I64, _P, _P, _I64, _P, _P, _I64, _I64, _I, _P, _P, _I,
+                                    _P, _I64, _P, _P, _I64, _P, _SZ, _P]),
+    "nm_sparse_densify": (_I, [_P, _P, _I64, _I64, _I, _I, _P, _I64, _P]),
+    "nm_sparse_gemm_lora_workspace_bytes": (_SZ, [_I64, _I64, _I, _I64, _I64, _I64]),
+    "nm_sparse_gemm_lora": (_I, [_P, _I64, _I64, _I64, _P, _I64, _I, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64,
+                                 _P, _P, _I64, _P, _I64, _P, _SZ, _P]),
 }
 
 _lock = threading.Lock()
@@ -418,6 +430,170 @@ def dense_gemm(X, W, Y=None, ws=None, stream=None):
         ws = _out(lib.nm_dense_gemm_workspace_bytes(T, K, R), dtype=torch.uint8, device=X.device)
     _check(lib.nm_dense_gemm(_ptr(X), T, K, _ld(X), _ptr(W), R, _ld(W), _ptr(Y), _ld(Y),
                              _ptr(ws), ws.numel(), _stream(stream)), "nm_dense_gemm")
+    return Y
+
+
+_ACTS = {"silu": 0, "gelu": 1, "relu2": 2}
+
+
+def _act(act):
+    if act not in _ACTS:
+        raise NMError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
+    return _ACTS[act]
+
+
+def _shape(t, name, *shape):
+    if tuple(t.shape) != shape:
+        raise NMError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    return t
+
+
+def _same_device(**tensors):
+    """Every tensor on one device, and that device the current one: the library
+    launches on the current device."""
+    devs = {t.device for t in tensors.values() if t is not None}
+    if len(devs) > 1:
+        raise NMError(f"{', '.join(tensors)} must be on one device, got {sorted(map(str, devs))}")
+    if devs != {torch.device("cuda", torch.cuda.current_device())}:
+        raise NMError(f"the tensors are on {devs.pop()}, not on the current device")
+
+
+def _packed(packed, R, K, m, name):
+    _dev(packed, name)
+    need = load().nm_sparse_prepare_bytes(R, K, m)
+    if need == 0:
+        raise NMError(f"unsupported shape or pattern (R={R}, K={K}, m={m})")
+    if not packed.is_contiguous() or packed.numel() * packed.element_size() < need:
+        raise NMError(f"{name} must be a contiguous operand of sparse_prepare(..., R={R}, K={K}, m={m})")
+    return packed
+
+
+def _on(stream):
+    """Context in which outputs and workspaces for a call on `stream` are made: the
+    caching allocator then hands their memory on in that stream's order."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+
+
+def _out_rows(T, R, device):
+    return _out((T, (R + 7) // 8 * 8), dtype=torch.bfloat16, device=device)[:, :R]
+
+
+def sparse_glu(X, packed_gate, packed_up, R, m, act="silu", save=False, H=None, ws=None, stream=None):
+    """H = act(X Wg^T) * (X Wu^T), both projections sparse, in one kernel; act is
+    "silu", "gelu" (tanh form) or "relu2".  save=True returns (H, G, U) with
+    G = X Wg^T and U = X Wu^T for sparse_glu_backward."""
+    X = _bf16(X, "X")
+    T, K = X.shape
+    a = _act(act)
+    _packed(packed_gate, R, K, m, "packed_gate")
+    _packed(packed_up, R, K, m, "packed_up")
+    _same_device(X=X, packed_gate=packed_gate, packed_up=packed_up, H=H, ws=ws)
+    lib = load()
+    G = U = None
+    with _on(stream):
+        H = _out_rows(T, R, X.device) if H is None else _shape(_bf16(H, "H"), "H", T, R)
+        if save:
+            G, U = _out_rows(T, R, X.device), _out_rows(T, R, X.device)
+        if ws is None:
+            ws = _out(lib.nm_sparse_glu_workspace_bytes(T, K, m), dtype=torch.uint8, device=X.device)
+    _check(lib.nm_sparse_glu(_ptr(X), T, K, _ld(X), _ptr(packed_gate), _ptr(packed_up), R, m, a, _ptr(H), _ld(H),
+                             _ptr(G), _ptr(U), _ld(G) if save else 0, _ptr(ws), ws.numel() * ws.element_size(),
+                             _stream(stream)), "nm_sparse_glu")
+    return (H, G, U) if save else H
+
+
+def sparse_glu_backward(dH, X, G, U, Wg, Wu, act="silu", mask_gate=None, mask_up=None, m=None, need_dx=True,
+                        need_dw=True, ws=None, stream=None):
+    """Gradients of sparse_glu: (dX, dWg, dWu), None for those not needed.  Wg and
+    Wu are the masked weights in dense form (sparse_densify).  Without masks
+    dWg and dWu go straight through to every weight; with the masks of
+    prune_compress (pattern width m) they are zero where the mask is."""
+    dH, G, U, Wg, Wu, X = (_bf16(t, n) for t, n in ((dH, "dH"), (G, "G"), (U, "U"), (Wg, "Wg"), (Wu, "Wu"), (X, "X")))
+    T, K = X.shape
+    R = Wg.shape[0]
+    a = _act(act)
+    for t, n, shape in ((dH, "dH", (T, R)), (G, "G", (T, R)), (U, "U", (T, R)), (Wg, "Wg", (R, K)), (Wu, "Wu", (R, K))):
+        _shape(t, n, *shape)
+    if (mask_gate is None) != (mask_up is None) or (mask_gate is not None and m is None):
+        raise NMError("mask_gate, mask_up and m go together")
+    if not need_dx and not need_dw:
+        raise NMError("nothing to compute: need_dx and need_dw are both false")
+    if mask_gate is not None:
+        for t, n in ((mask_gate, "mask_gate"), (mask_up, "mask_up")):
+            _shape(_dev(t, n), n, R, (n_groups(K, m) * m + 31) // 32)
+            if t.element_size() != 4 or not t.is_contiguous():
+                raise NMError(f"{n} must be contiguous 32-bit words")
+    _same_device(dH=dH, X=X, G=G, U=U, Wg=Wg, Wu=Wu, mask_gate=mask_gate, mask_up=mask_up, ws=ws)
+    if _ld(G) != _ld(U) or _ld(Wg) != _ld(Wu):
+        raise NMError("G and U, and Wg and Wu, must have the same row stride")
+    lib = load()
+    with _on(stream):
+        dX = _out_rows(T, K, X.device) if need_dx else None
+        dWg, dWu = (_out_rows(R, K, X.device), _out_rows(R, K, X.device)) if need_dw else (None, None)
+        if ws is None:
+            ws = _out(lib.nm_sparse_glu_backward_workspace_bytes(T, R), dtype=torch.uint8, device=X.device)
+    _check(lib.nm_sparse_glu_backward(_ptr(dH), _ld(dH), _ptr(X), T, K, _ld(X), _ptr(G), _ptr(U), _ld(G), _ptr(Wg),
+                                      _ptr(Wu), R, _ld(Wg), a, _ptr(mask_gate), _ptr(mask_up), m or 0, _ptr(dX),
+                                      _ld(dX) if need_dx else 0, _ptr(dWg), _ptr(dWu), _ld(dWg) if need_dw else 0,
+                                      _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "nm_sparse_glu_backward")
+    return dX, dWg, dWu
+
+
+def sparse_densify(vals, mask, R, K, n, m, W=None, stream=None):
+    """mask (.) V in dense form, bf16 [R x K], from prune_compress's kept values
+    and mask."""
+    vals = _bf16(vals, "vals")
+    _dev(mask, "mask")
+    if not 1 <= n < m <= 16:
+        raise NMError(f"unsupported pattern {n}:{m}")
+    _shape(vals, "vals", R, n_groups(K, m) * n)
+    _shape(mask, "mask", R, (n_groups(K, m) * m + 31) // 32)
+    if not vals.is_contiguous() or not mask.is_contiguous() or mask.element_size() != 4:
+        raise NMError("vals and mask must be contiguous, mask of 32-bit words")
+    _same_device(vals=vals, mask=mask, W=W)
+    with _on(stream):
+        W = _out_rows(R, K, vals.device) if W is None else _shape(_bf16(W, "W"), "W", R, K)
+    _check(load().nm_sparse_densify(_ptr(vals), _ptr(mask), R, K, n, m, _ptr(W), _ld(W), _stream(stream)),
+           "nm_sparse_densify")
+    return W
+
+
+def sparse_gemm_lora(X, packed, R, m, A, B, scale, indptr, ids, Y=None, ws=None, stream=None):
+    """Y = X * W_sparse^T plus, for the tokens indptr[i] .. indptr[i+1] of request
+    i, scale[a] (X A[a]^T) B[a]^T with a = ids[i] (-1: no adapter).  A
+    [adapters x r x K], B [adapters x R x r] bf16, scale fp32 [adapters],
+    indptr int32 [requests + 1], ids int32 [requests], all on the device."""
+    X, A, B = _bf16(X, "X"), _bf16(A, "A"), _bf16(B, "B")
+    T, K = X.shape
+    if A.dim() != 3 or B.dim() != 3:
+        raise NMError("A and B must be [adapters x r x K] and [adapters x R x r]")
+    n, r = A.shape[:2]
+    _shape(A, "A", n, r, K)
+    _shape(B, "B", n, R, r)
+    _packed(packed, R, K, m, "packed")
+    for t, name, dtype in ((scale, "scale", torch.float32), (indptr, "indptr", torch.int32), (ids, "ids", torch.int32)):
+        _dev(t, name)
+        if t.dtype != dtype or t.dim() != 1 or not t.is_contiguous():
+            raise NMError(f"{name} must be a contiguous 1-D tensor of {dtype}")
+    q = ids.shape[0]
+    _shape(scale, "scale", n)
+    _shape(indptr, "indptr", q + 1)
+    _same_device(X=X, packed=packed, A=A, B=B, scale=scale, indptr=indptr, ids=ids, Y=Y, ws=ws)
+    lib = load()
+    need = lib.nm_sparse_gemm_lora_workspace_bytes(T, K, m, r, n, q)
+    if need == 0:
+        raise NMError(f"unsupported adapters (r={r}: a multiple of 8 up to 256; {n} of them)")
+    with _on(stream):
+        Y = _out_rows(T, R, X.device) if Y is None else _shape(_bf16(Y, "Y"), "Y", T, R)
+        if ws is None:
+            ws = _out(need, dtype=torch.uint8, device=X.device)
+    _check(lib.nm_sparse_gemm_lora(_ptr(X), T, K, _ld(X), _ptr(packed), R, m, _ptr(A), A.stride(1), A.stride(0),
+                                   _ptr(B), B.stride(1), B.stride(0), _ptr(scale), n, r, _ptr(indptr), _ptr(ids), q,
+                                   _ptr(Y), _ld(Y), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
+           "nm_sparse_gemm_lora")
     return Y
 
 

@@ -52,6 +52,22 @@ inline bool make_tmap_bf16(CUtensorMap *map, const void *base, int64_t rows, int
                         box_rows, swizzle128);
 }
 
+// 3-D tensor map over `depth` row-major bf16 matrices [rows x cols] (row stride
+// ld, matrix stride sd elements), 128-byte swizzle, boxes of one matrix
+inline bool make_tmap_bf16_3d(CUtensorMap *map, const void *base, int64_t depth, int64_t rows, int64_t cols,
+                              int64_t ld, int64_t sd, uint32_t box_cols, uint32_t box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
+                          static_cast<cuuint64_t>(depth)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(sd) * 2};
+    cuuint32_t box[3] = {box_cols, box_rows, 1};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // raises a kernel's dynamic shared-memory limit once per device
 template <auto kernel>
 inline bool set_smem_attr(int bytes) {
