@@ -344,6 +344,12 @@ __device__ __forceinline__ double ld_dsmem_f64(uint32_t cluster_addr) {
     return v;
 }
 
+__device__ __forceinline__ float ld_dsmem_f32(uint32_t cluster_addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
 __device__ __forceinline__ void cluster_sync_all() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                      : "memory");
@@ -450,6 +456,15 @@ __device__ __forceinline__ void mma_sp_bf16_pair(uint32_t d_tmem, uint64_t a_des
 // commit of a pair MMA: arrive on the barrier at this offset in both CTAs
 __device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
     const uint16_t mask = 0x3;
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+        " [%0], %1;" ::"r"(smem_u32(bar)),
+        "h"(mask)
+        : "memory");
+}
+
+// the same for a pair inside a larger cluster: `mask` has the bits of its two CTAs
+__device__ __forceinline__ void mma_commit_pair_mask(uint64_t *bar, uint16_t mask) {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
         " [%0], %1;" ::"r"(smem_u32(bar)),

@@ -37,27 +37,18 @@ struct FfnCfg {
     static constexpr int OFF_A0 = 0, OFF_A1 = A_BYTES, OFF_E0 = 2 * A_BYTES, OFF_E1 = OFF_E0 + EBLK_BYTES;
     static constexpr int OFF_B = OFF_E1 + EBLK_BYTES;  // two atoms of bn/2 tokens x 64 columns
     static constexpr int MAX_STAGES = 6;
+    static constexpr int MAX_SPLIT = 8;         // CTA pairs that share a tile's K' blocks
     static constexpr int EPI_WARPS = 8;
     static constexpr int THREADS = 384;
     static constexpr int BAR_BYTES = 256;
     static constexpr int SMEM_BYTES = 232448;
-    static constexpr int SMEM_STAGES = SMEM_BYTES - BAR_BYTES - 1024;
+    static constexpr int SMEM_DATA = (SMEM_BYTES - BAR_BYTES - 1024) / 1024 * 1024;
     static constexpr int TMEM_COLS = 512;
     static constexpr int TMEM_D0 = 0, TMEM_E0 = 240, TMEM_E1 = 248, TMEM_D1 = 256;
     static_assert(OFF_B % 1024 == 0, "operand alignment");
     static int stage_bytes(int bn) { return OFF_B + bn * 128; }
-    static int stages(int bn) {
-        const int s = SMEM_STAGES / stage_bytes(bn);
-        return s < MAX_STAGES ? s : MAX_STAGES;
-    }
+    static int sum_bytes(int bn) { return bn * 1024; }  // both accumulators of a CTA in fp32
 };
-
-// stream-K slot of one epilogue warp: 32 rows x up to 256 columns (OP_GLU: 128
-// of each accumulator), [column][row]
-constexpr int FFN_SLOT_FLOATS = 32 * 256;
-inline size_t ffn_sk_bytes(int64_t pairs) {
-    return static_cast<size_t>(pairs) * 2 * 8 * (FFN_SLOT_FLOATS * 4 + 8);
-}
 
 struct FfnMaps {
     CUtensorMap a0, a1, e0, e1;  // values and metadata of the two accumulators' weights
@@ -68,17 +59,16 @@ struct FfnMaps {
 struct FfnArgs {
     int64_t T, R, nkb;
     int bn, stages, stage_bytes;
-    int early;  // loads of X and the weights need not wait for the preceding kernel
+    int split;    // CTA pairs of a cluster that share a tile
+    int sum_off;  // split > 1: where a CTA leaves its fp32 sums in shared memory
+    int early;    // loads of X and the weights need not wait for the preceding kernel
     uint16_t *Y, *G, *U;
     int64_t ldy, ldgu;
     int act;
     // OP_LORA: adapters per token tile, the tile's first slot, a slot's adapter;
-    // at most ext_cap slots per tile, rb blocks of 64 ranks per slot
+    // rb blocks of 64 ranks per slot; tile_cnt NULL: no adapters at all
     const int32_t *tile_cnt, *tile_base, *slot_adapter;
-    int ext_cap, rb;
-    uint8_t *sk_ws;
-    uint64_t seq;
-    int sk;
+    int rb;
 };
 
 __device__ __forceinline__ float act_of(float g, int act) {
@@ -89,23 +79,31 @@ __device__ __forceinline__ float act_of(float g, int act) {
     return __fdividef(g, 1.0f + __expf(-z));
 }
 
+// A cluster of `split` pairs computes a tile: pair j takes the j-th part of its
+// K' blocks (and of its adapters' blocks).  With split > 1 every CTA leaves the
+// fp32 sums of its 128 + 128 rows in shared memory, and pair j adds the parts
+// of all pairs for its share of the tokens, reading them through distributed
+// shared memory in the pairs' order (so results do not depend on timing), and
+// finishes those tokens.  Nothing goes through global memory and nothing
+// outlives the launch.
 template <int MODE, int OP>
 __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
     k_ffn(const __grid_constant__ FfnMaps tm, const __grid_constant__ FfnArgs p) {
     using C = FfnCfg;
     const int S = p.stages;
-    const bool sk = p.sk != 0;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::SMEM_STAGES / 1024 * 1024);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::SMEM_DATA);
     uint64_t *full = bars, *empty = bars + C::MAX_STAGES;
     uint64_t *acc_full = bars + 2 * C::MAX_STAGES, *acc_empty = acc_full + 1;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_full + 2);
+    uint64_t *sum_ready = acc_full + 2, *sum_free = acc_full + 3;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_full + 4);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
-    const int64_t cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
+    const uint32_t crank = cluster_ctarank(), rank = crank & 1u, leader = crank & ~1u;
+    const int split = p.split, part = static_cast<int>(crank >> 1);
+    const int64_t cluster = blockIdx.x / (2 * split), nclusters = gridDim.x / (2 * split);
     const int bn = p.bn, bh = bn >> 1;
     const int b_atom = bh * 128;
     const int64_t nkb = p.nkb, T = p.T;
@@ -114,11 +112,16 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
     const int64_t n_t = (T + bn - 1) / bn;
     const int64_t n_m = (Rpad + TILE_ROWS - 1) / TILE_ROWS;
     const int64_t ntiles = n_t * n_m;
-    const int64_t nkt = OP == OP_LORA ? nkb + static_cast<int64_t>(p.ext_cap) * p.rb : nkb;
+    const int64_t kb0 = nkb * part / split, kb1 = nkb * (part + 1) / split;  // this pair's K' blocks
     auto stage = [&](int s) { return smem + s * p.stage_bytes; };
-    // K' blocks of a tile: the projection's, then rb per adapter among its tokens
-    auto tile_blocks = [&](int64_t nt) -> int64_t {
-        return OP == OP_LORA && p.ext_cap > 0 ? nkb + static_cast<int64_t>(__ldcg(p.tile_cnt + nt)) * p.rb : nkb;
+    // this pair's blocks of the adapters of token tile nt
+    auto adapter_blocks = [&](int64_t nt, int &x0, int &x1) {
+        x0 = x1 = 0;
+        if (OP == OP_LORA && p.tile_cnt != nullptr) {
+            const int n = __ldcg(p.tile_cnt + nt) * p.rb;
+            x0 = n * part / split;
+            x1 = n * (part + 1) / split;
+        }
     };
 
     if (threadIdx.x == 0) {
@@ -128,6 +131,8 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
         }
         mbar_init(acc_full, 1);
         mbar_init(acc_empty, 2 * C::EPI_WARPS);
+        mbar_init(sum_ready, split * C::EPI_WARPS);
+        mbar_init(sum_free, split * C::EPI_WARPS);
         fence_barrier_init();
         prefetch_tmap(&tm.a0);
         prefetch_tmap(&tm.e0);
@@ -160,10 +165,13 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
             uint32_t ph = 0;
             int64_t it = 0;
             bool ok = true, dep_done = p.early == 0;
-            SegIter seg(sk, cluster, nclusters, ntiles, nkt);
-            int64_t tile, kb0, kb1;
             const uint32_t b_bytes = 2u * static_cast<uint32_t>(b_atom);
-            while (ok && seg.next(tile, kb0, kb1)) {
+            const CUtensorMap *ta1 = OP == OP_GLU ? &tm.a1 : &tm.a0, *te1 = OP == OP_GLU ? &tm.e1 : &tm.e0;
+            auto advance = [&]() {
+                ++it;
+                if (++s == S) { s = 0; ph ^= 1u; }
+            };
+            for (int64_t tile = cluster; tile < ntiles && ok; tile += nclusters) {
                 int64_t nt, mt;
                 tile_coords(tile, n_t, n_m, BAND_ROWS / TILE_ROWS, nt, mt);
                 const bool has1 = OP == OP_GLU || mt * 512 + 256 < Rpad;
@@ -172,56 +180,53 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
                 const int32_t brow = static_cast<int32_t>(nt * bn + rank * bh);
                 const int64_t e0 = (arow >> 7) * nkb, e1 = (arow1 >> 7) * nkb;
                 const uint32_t tx = 2u * ((has1 ? 2u : 1u) * (C::A_BYTES + EBLK_BYTES) + b_bytes);
-                const CUtensorMap *ta1 = OP == OP_GLU ? &tm.a1 : &tm.a0, *te1 = OP == OP_GLU ? &tm.e1 : &tm.e0;
-                int64_t vend = kb1;                // the tile's blocks that this segment runs
-                int32_t slot0 = 0, a_next = 0;     // its first slot; the next block's adapter
-                bool adapters_known = false;
-                for (int64_t v = kb0; v < vend; ++v) {
-                    const bool ext = OP == OP_LORA && v >= nkb;
-                    const int64_t kb = ext ? v : (MODE == PMODE_SP68T ? visit68(v, nkb) : v);
-                    const bool mid = MODE == PMODE_SP68T && !ext && (kb % 3) == 2;
-                    if ((mid || ext) && !dep_done) {  // written by the kernels just before
+                for (int64_t v = kb0; v < kb1; ++v) {
+                    const int64_t kb = MODE == PMODE_SP68T ? visit68(v, nkb) : v;
+                    const bool mid = MODE == PMODE_SP68T && (kb % 3) == 2;
+                    if (mid && !dep_done) {  // written by the kernel just before
                         grid_dep_wait();
                         dep_done = true;
                     }
-                    if (ext && !adapters_known) {
-                        adapters_known = true;
-                        const int64_t nb = tile_blocks(nt);
-                        if (nb < vend) vend = nb;
-                        if (v >= vend) break;
-                        slot0 = __ldcg(p.tile_base + nt);
-                        a_next = __ldcg(p.slot_adapter + slot0 + static_cast<int>(v - nkb) / p.rb);
-                    }
                     if (it >= S && !mbar_wait(&empty[s], ph ^ 1u)) { ok = false; break; }
-                    const uint32_t bar = mapa_shared(&full[s], 0);
+                    if (rank == 0) mbar_arrive_expect_tx(&full[s], tx);
+                    const uint32_t bar = mapa_shared(&full[s], leader);
                     uint8_t *st = stage(s);
-                    if (ext) {
-                        const int slot = static_cast<int>(v - nkb) / p.rb;
-                        const int32_t rk = static_cast<int32_t>((v - nkb) - static_cast<int64_t>(slot) * p.rb) * 64;
-                        const int32_t gs = slot0 + slot, a = a_next;
-                        if (v + 1 < vend) a_next = __ldcg(p.slot_adapter + slot0 + static_cast<int>(v + 1 - nkb) / p.rb);
+                    const int32_t ka = static_cast<int32_t>(kb * 64);
+                    tma_load_2d_pair(st + C::OFF_A0, &tm.a0, bar, ka, arow);
+                    tma_load_2d_pair(st + C::OFF_E0, &tm.e0, bar, 0, static_cast<int32_t>((e0 + kb) * 8));
+                    if (has1) {
+                        tma_load_2d_pair(st + C::OFF_A1, ta1, bar, ka, arow1);
+                        tma_load_2d_pair(st + C::OFF_E1, te1, bar, 0, static_cast<int32_t>((e1 + kb) * 8));
+                    }
+                    const int64_t xc = MODE == PMODE_SP24 ? kb * 128
+                                       : (mid ? (kb / 3) * 128 : (kb / 3) * 256 + (kb % 3) * 128);
+                    const CUtensorMap *tb = mid ? &tm.b2 : &tm.b;
+                    tma_load_2d_pair(st + C::OFF_B, tb, bar, static_cast<int32_t>(xc), brow);
+                    tma_load_2d_pair(st + C::OFF_B + b_atom, tb, bar, static_cast<int32_t>(xc + 64), brow);
+                    advance();
+                }
+                if (OP == OP_LORA && ok && p.tile_cnt != nullptr) {
+                    if (!dep_done) {
+                        grid_dep_wait();
+                        dep_done = true;
+                    }
+                    int x0, x1;
+                    adapter_blocks(nt, x0, x1);
+                    const int32_t slot0 = __ldcg(p.tile_base + nt);
+                    int32_t a_next = x0 < x1 ? __ldcg(p.slot_adapter + slot0 + x0 / p.rb) : 0;
+                    for (int x = x0; x < x1; ++x) {
+                        const int32_t a = a_next, slot = slot0 + x / p.rb, rk = (x % p.rb) * 64;
+                        if (x + 1 < x1) a_next = __ldcg(p.slot_adapter + slot0 + (x + 1) / p.rb);
+                        if (it >= S && !mbar_wait(&empty[s], ph ^ 1u)) { ok = false; break; }
                         if (rank == 0)
                             mbar_arrive_expect_tx(&full[s], 2u * ((has1 ? 2u : 1u) * C::A_BYTES + b_bytes / 2));
+                        const uint32_t bar = mapa_shared(&full[s], leader);
+                        uint8_t *st = stage(s);
                         tma_load_3d_pair(st + C::OFF_A0, &tm.lb, bar, rk, arow, a);
                         if (has1) tma_load_3d_pair(st + C::OFF_A1, &tm.lb, bar, rk, arow + 256, a);
-                        tma_load_2d_pair(st + C::OFF_B, &tm.lv, bar, rk, gs * bn + static_cast<int32_t>(rank) * bh);
-                    } else {
-                        if (rank == 0) mbar_arrive_expect_tx(&full[s], tx);
-                        const int32_t ka = static_cast<int32_t>(kb * 64);
-                        tma_load_2d_pair(st + C::OFF_A0, &tm.a0, bar, ka, arow);
-                        tma_load_2d_pair(st + C::OFF_E0, &tm.e0, bar, 0, static_cast<int32_t>((e0 + kb) * 8));
-                        if (has1) {
-                            tma_load_2d_pair(st + C::OFF_A1, ta1, bar, ka, arow1);
-                            tma_load_2d_pair(st + C::OFF_E1, te1, bar, 0, static_cast<int32_t>((e1 + kb) * 8));
-                        }
-                        const int64_t x0 = MODE == PMODE_SP24 ? kb * 128
-                                           : (mid ? (kb / 3) * 128 : (kb / 3) * 256 + (kb % 3) * 128);
-                        const CUtensorMap *tb = mid ? &tm.b2 : &tm.b;
-                        tma_load_2d_pair(st + C::OFF_B, tb, bar, static_cast<int32_t>(x0), brow);
-                        tma_load_2d_pair(st + C::OFF_B + b_atom, tb, bar, static_cast<int32_t>(x0 + 64), brow);
+                        tma_load_2d_pair(st + C::OFF_B, &tm.lv, bar, rk, slot * bn + static_cast<int32_t>(rank) * bh);
+                        advance();
                     }
-                    ++it;
-                    if (++s == S) { s = 0; ph ^= 1u; }
                 }
             }
             if (!ok && rank == 0) {  // let copies already issued land before exiting
@@ -234,25 +239,20 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
         if (rank == 0 && lane == 0) {
             const uint32_t idesc = make_idesc_bf16(256, bn, true, 0);
             const uint32_t idesc_dense = make_idesc_bf16(256, bn, false, 0);
+            const uint16_t both = static_cast<uint16_t>(3u << leader);
             int s = 0;
             uint32_t ph = 0;
             int64_t ti = 0;
             bool ok = true, dep_done = p.early == 0;
-            SegIter seg(sk, cluster, nclusters, ntiles, nkt);
-            int64_t tile, kb0, kb1;
-            for (; ok && seg.next(tile, kb0, kb1); ++ti) {
+            for (int64_t tile = cluster; tile < ntiles && ok; tile += nclusters, ++ti) {
                 int64_t nt, mt;
                 tile_coords(tile, n_t, n_m, BAND_ROWS / TILE_ROWS, nt, mt);
                 const bool has1 = OP == OP_GLU || mt * 512 + 256 < Rpad;
-                if (ti >= 1 && !mbar_wait_cluster(acc_empty, static_cast<uint32_t>((ti - 1) & 1))) {
-                    ok = false;
-                    break;
-                }
+                if (ti >= 1 && !mbar_wait_cluster(acc_empty, static_cast<uint32_t>((ti - 1) & 1))) break;
                 tc_fence_after();
                 const uint32_t d0 = tmem_base + C::TMEM_D0, d1 = tmem_base + C::TMEM_D1;
                 const uint32_t te0 = tmem_base + C::TMEM_E0, te1 = tmem_base + C::TMEM_E1;
-                const int64_t base_end = OP == OP_LORA && kb1 > nkb ? nkb : kb1;
-                for (int64_t kb = kb0; kb < base_end; ++kb) {
+                for (int64_t kb = kb0; kb < kb1; ++kb) {
                     if (!mbar_wait(&full[s], ph)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t st = smem_u32(stage(s));
@@ -269,53 +269,44 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
                             mma_sp_bf16_pair(d1, make_sdesc(st + C::OFF_A1 + j * 32, 16, 1024, 2), bd,
                                              te1 + (j & ~1), id, acc);
                     }
-                    mma_commit_pair(&empty[s]);
+                    mma_commit_pair_mask(&empty[s], both);
                     if (++s == S) { s = 0; ph ^= 1u; }
                 }
-                if (OP == OP_LORA && ok && kb1 > nkb) {
+                if (OP == OP_LORA && ok && p.tile_cnt != nullptr) {
                     if (!dep_done) {
                         grid_dep_wait();
                         dep_done = true;
                     }
-                    const int64_t nb = tile_blocks(nt), end = nb < kb1 ? nb : kb1;
-                    for (int64_t v = kb0 > nkb ? kb0 : nkb; v < end; ++v) {
+                    int x0, x1;
+                    adapter_blocks(nt, x0, x1);
+                    for (int x = x0; x < x1; ++x) {  // on top of this pair's K' blocks
                         if (!mbar_wait(&full[s], ph)) { ok = false; break; }
                         tc_fence_after();
                         const uint32_t st = smem_u32(stage(s));
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const uint64_t bd = make_sdesc(st + C::OFF_B + j * 32, 16, 1024, 2);
-                            const uint32_t acc = (v > kb0 || j > 0) ? 1u : 0u;
-                            mma_bf16_pair(d0, make_sdesc(st + C::OFF_A0 + j * 32, 16, 1024, 2), bd, idesc_dense, acc);
+                            mma_bf16_pair(d0, make_sdesc(st + C::OFF_A0 + j * 32, 16, 1024, 2), bd, idesc_dense, 1u);
                             if (has1)
                                 mma_bf16_pair(d1, make_sdesc(st + C::OFF_A1 + j * 32, 16, 1024, 2), bd, idesc_dense,
-                                              acc);
+                                              1u);
                         }
-                        mma_commit_pair(&empty[s]);
+                        mma_commit_pair_mask(&empty[s], both);
                         if (++s == S) { s = 0; ph ^= 1u; }
                     }
                 }
-                if (ok) mma_commit_pair(acc_full);
+                if (ok) mma_commit_pair_mask(acc_full, both);
             }
         }
     } else if (warp >= 4 && warp < 12) {
         // ---------------------------------------------------------- epilogue
         // OP_GLU : warp = lane quarter q x token half h, both accumulators
         // OP_LORA: warp = lane quarter q x accumulator h, all tokens
-        const int q = warp & 3, h = (warp - 4) >> 2, we = warp - 4;
+        const int q = warp & 3, h = (warp - 4) >> 2;
         constexpr int NACC = OP == OP_GLU ? 2 : 1;
-        const uint32_t acc_empty_cl = mapa_shared(acc_empty, 0);
-        float *slots = reinterpret_cast<float *>(p.sk_ws);
-        uint64_t *flags = reinterpret_cast<uint64_t *>(p.sk_ws + static_cast<size_t>(nclusters) * 2 * 8 *
-                                                                     FFN_SLOT_FLOATS * 4);
-        const int64_t total = ntiles * nkt;
-        auto has_work = [&](int64_t cc) { return (cc + 1) * total / nclusters > cc * total / nclusters; };
-        auto slot_of = [&](int64_t cc) {
-            return slots + static_cast<size_t>((cc * 2 + rank) * 8 + we) * FFN_SLOT_FLOATS + lane;
-        };
-        SegIter seg(sk, cluster, nclusters, ntiles, nkt);
-        int64_t tile, kb0, kb1, ti = 0;
-        for (; seg.next(tile, kb0, kb1); ++ti) {
+        const uint32_t acc_empty_cl = mapa_shared(acc_empty, leader);
+        int64_t ti = 0;
+        for (int64_t tile = cluster; tile < ntiles; tile += nclusters, ++ti) {
             int64_t nt, mt;
             tile_coords(tile, n_t, n_m, BAND_ROWS / TILE_ROWS, nt, mt);
             if (!__all_sync(0xffffffffu, mbar_wait(acc_full, static_cast<uint32_t>(ti & 1)))) break;
@@ -326,19 +317,21 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
             const int nv = static_cast<int>(T - tok0 < bn ? T - tok0 : bn);  // real tokens of the tile
             const int nch = (nv + 15) / 16;                                  // their chunks of 16
             int c_lo = 0, c_hi = nch;
+            const bool active = OP == OP_GLU || h == 0 || mt * 512 + 256 < Rpad;
             if (OP == OP_GLU) {
                 const int half = (bn / 16 + 1) / 2;
                 c_lo = h ? half : 0;
                 c_hi = h ? nch : (nch < half ? nch : half);
-            } else if (h && mt * 512 + 256 >= Rpad) {
+            } else if (!active) {
                 c_hi = 0;
             }
-            if (sk && kb0 > 0) {
-                // later part of a split tile: the fp32 partial (real tokens) goes to
-                // the owner.  A range that holds only blocks of absent adapters ran
-                // no MMA: its part is zero, not what tensor memory holds.
-                const bool none = OP == OP_LORA && kb0 >= tile_blocks(nt);
-                float *slot = slot_of(cluster);
+            const int64_t row = mt * TILE_ROWS + (OP == OP_LORA ? h * 256 : 0) + rank * 128 + q * 32 + lane;
+            const bool rok = row < p.R;
+            if (split > 1) {
+                // [accumulator][token][row] fp32 in this CTA's shared memory
+                float *mine = reinterpret_cast<float *>(smem + p.sum_off) + q * 32 + lane;
+                if (ti >= 1 && !__all_sync(0xffffffffu, mbar_wait_cluster(sum_free, static_cast<uint32_t>((ti - 1) & 1))))
+                    break;
 #pragma unroll 1
                 for (int c = c_lo; c < c_hi; ++c) {
                     uint32_t v[NACC][16];
@@ -349,42 +342,62 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
                     for (int a = 0; a < NACC; ++a)
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            if (c * 16 + j < nv)
-                                __stcg(slot + (((c - c_lo) * NACC + a) * 16 + j) * 32,
-                                       none ? 0.0f : __uint_as_float(v[a][j]));
+                            mine[((OP == OP_GLU ? a : h) * bn + c * 16 + j) * 128] = __uint_as_float(v[a][j]);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(acc_empty_cl);
-                __threadfence();
+                if (lane < split) mbar_arrive_cluster(mapa_shared(sum_ready, 2 * lane + rank));
+                if (!__all_sync(0xffffffffu, mbar_wait_cluster(sum_ready, static_cast<uint32_t>(ti & 1)))) break;
+                // this pair's tokens, every second one to each half of the warps
+                // (OP_GLU) or all of them to each accumulator's (OP_LORA)
+                constexpr int STEP = OP == OP_GLU ? 2 : 1;
+                const int t1 = active ? nv * (part + 1) / split : 0;
+                const uint32_t off = smem_u32(mine);
+                uint32_t from[C::MAX_SPLIT];
+#pragma unroll
+                for (int i = 0; i < C::MAX_SPLIT; ++i) {
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                                 : "=r"(from[i]) : "r"(off), "r"(2 * (i < split ? i : part) + rank));
+                }
+#pragma unroll 1
+                for (int t = nv * part / split + (OP == OP_GLU ? h : 0); t < t1; t += 2 * STEP) {
+                    float f[NACC][2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int tt = t + u * STEP < t1 ? t + u * STEP : t;
+#pragma unroll
+                        for (int a = 0; a < NACC; ++a) {
+                            const uint32_t at = static_cast<uint32_t>(((OP == OP_GLU ? a : h) * bn + tt) * 512);
+                            float pv[C::MAX_SPLIT];
+#pragma unroll
+                            for (int i = 0; i < C::MAX_SPLIT; ++i)
+                                pv[i] = i < split ? ld_dsmem_f32(from[i] + at) : 0.0f;
+                            f[a][u] = pv[0];
+#pragma unroll
+                            for (int i = 1; i < C::MAX_SPLIT; ++i)
+                                if (i < split) f[a][u] += pv[i];
+                        }
+                    }
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const int64_t tk = tok0 + t + u * STEP;
+                        if (t + u * STEP < t1 && rok) {
+                            if (OP == OP_GLU) {
+                                if (p.G != nullptr) {
+                                    p.G[tk * p.ldgu + row] = static_cast<uint16_t>(pack_bf16x2(f[0][u], 0.0f));
+                                    p.U[tk * p.ldgu + row] = static_cast<uint16_t>(pack_bf16x2(f[NACC - 1][u], 0.0f));
+                                }
+                                f[0][u] = act_of(f[0][u], p.act) * f[NACC - 1][u];
+                            }
+                            p.Y[tk * p.ldy + row] = static_cast<uint16_t>(pack_bf16x2(f[0][u], 0.0f));
+                        }
+                    }
+                }
                 __syncwarp();
-                if (lane == 0 && cluster != g_test_withhold_flag_cluster)
-                    st_release_u64(flags + (cluster * 2 + rank) * 8 + we, p.seq);
+                if (lane < split) mbar_arrive_cluster(mapa_shared(sum_free, 2 * lane + rank));
                 continue;
             }
-            int64_t last_contrib = cluster;
-            if (sk && kb1 < nkt) {
-                // owner of a split tile (always this cluster's last segment): wait for
-                // the clusters after this one that hold the rest, each lane polling one
-                // flag, and clear it once seen, so that a replay of the same launch
-                // (the same sequence number) waits for its own partial sums
-                while (last_contrib + 1 < nclusters &&
-                       (last_contrib + 1) * total / nclusters < (tile + 1) * nkt)
-                    ++last_contrib;
-                bool got = true;
-                for (int64_t base = cluster + 1; base <= last_contrib && got; base += 32) {
-                    const int64_t cc = base + lane;
-                    bool mine = true;
-                    if (cc <= last_contrib && has_work(cc)) {
-                        uint64_t *fl = flags + (cc * 2 + rank) * 8 + we;
-                        mine = sk_wait_flag(fl, p.seq);
-                        if (mine) *reinterpret_cast<volatile uint64_t *>(fl) = 0;
-                    }
-                    got = __all_sync(0xffffffffu, mine);
-                }
-            }
-            const int64_t row = mt * TILE_ROWS + (OP == OP_LORA ? h * 256 : 0) + rank * 128 + q * 32 + lane;
-            const bool rok = row < p.R;
             uint32_t pk[8][8];
             // two passes of eight chunks (OP_GLU: one); the accumulator is released
             // once the last chunk is in registers, before its stores
@@ -403,17 +416,6 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
                         for (int a = 0; a < NACC; ++a)
 #pragma unroll
                             for (int j = 0; j < 16; ++j) f[a][j] = __uint_as_float(v[a][j]);
-                        if (last_contrib > cluster) {
-                            for (int64_t cc = cluster + 1; cc <= last_contrib; ++cc) {
-                                if (!has_work(cc)) continue;
-                                const float *ps = slot_of(cc) + (c - c_lo) * NACC * 16 * 32;
-#pragma unroll
-                                for (int a = 0; a < NACC; ++a)
-#pragma unroll
-                                    for (int j = 0; j < 16; ++j)
-                                        if (c * 16 + j < nv) f[a][j] += __ldcg(ps + (a * 16 + j) * 32);
-                            }
-                        }
                         if (OP == OP_GLU) {
                             const int64_t t = tok0 + c * 16;
                             if (p.G != nullptr && rok) {
@@ -421,7 +423,7 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
 #pragma unroll
                                 for (int j = 0; j < 16; j += 2) {
                                     const uint32_t g2 = pack_bf16x2(f[0][j], f[0][j + 1]);
-                                    const uint32_t u2 = pack_bf16x2(f[1][j], f[1][j + 1]);
+                                    const uint32_t u2 = pack_bf16x2(f[NACC - 1][j], f[NACC - 1][j + 1]);
                                     if (c * 16 + j < nv) {
                                         gp[j * p.ldgu] = static_cast<uint16_t>(g2 & 0xFFFFu);
                                         up[j * p.ldgu] = static_cast<uint16_t>(u2 & 0xFFFFu);
@@ -464,7 +466,7 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();
+    cluster_sync_all();  // also: no CTA leaves while another reads its sums
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
@@ -478,78 +480,23 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
 // indptr[i+1]) and adapter ids[i] (-1: none); tokens behind the last request
 // have none.  A slot is one (token tile, adapter that occurs in it); its V is
 // [bn x r], zero in the rows of other tokens.  Tile i's slots start at i * cap
-// (few adapters) or at i + (the request of its first token): along the batch
+// (few adapters) or at i + (the requests that end before it): along the batch
 // each tile or request border starts at most one new pair, so that numbering
 // leaves every tile room and needs requests + tiles slots in all.
+//
+// k_lora_shrink, one (tile, chunk of 32 tokens, rank block of <= 64) per
+// cluster of SHRINK_PARTS blocks that split K.  Every block first works out its
+// tile's slots (one pass over the list, a hash of the adapters; about a
+// microsecond, less than a kernel of its own would take to start), then, for
+// each slot z, z + gridDim.z, ..: the warps run mma.sync over blocks of 32
+// columns; a thread's 16-byte loads of X and A cover the same eight columns,
+// which the two k-steps of a block take in a permuted order (the same one for
+// both operands).  The warps' and then the blocks' fp32 sums are added in a
+// fixed order, through shared and distributed shared memory.
 // ---------------------------------------------------------------------------
-__global__ void __launch_bounds__(256)
-    k_lora_plan(const int32_t *__restrict__ indptr, const int32_t *__restrict__ ids, int32_t requests,
-                int32_t adapters, int64_t T, int bn, int cap, int by_cap, int64_t nslots,
-                int32_t *__restrict__ token_slot, int32_t *__restrict__ tile_cnt,
-                int32_t *__restrict__ tile_base, int32_t *__restrict__ slot_adapter) {
-    __shared__ int32_t adp[256];
-    __shared__ int32_t slot_at[256];
-    __shared__ int32_t warp_cnt[8];
-    __shared__ int32_t first_q;
-    grid_dep_launch();
-    const int tile = blockIdx.x, i = threadIdx.x, warp = i >> 5, lane = i & 31;
-    const int64_t t = static_cast<int64_t>(tile) * bn + i;
-    bool bad = false;
-    if (tile == 0) {  // the whole list once: ascending, within [0, T], known adapters
-        for (int q = i; q < requests; q += 256) {
-            const int32_t lo = __ldg(indptr + q), hi = __ldg(indptr + q + 1), a = __ldg(ids + q);
-            bad |= lo < 0 || lo > hi || hi > T || a < -1 || a >= adapters;
-        }
-    }
-    int32_t a = -1;
-    if (i < bn && t < T) {
-        int lo = 0, hi = requests;  // the first request that ends behind t
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (__ldg(indptr + mid + 1) > t) hi = mid; else lo = mid + 1;
-        }
-        if (lo < requests && __ldg(indptr + lo) <= t) {
-            a = __ldg(ids + lo);
-            if (a < 0 || a >= adapters) a = -1;
-        }
-        if (i == 0) first_q = lo;
-    }
-    adp[i] = a;
-    __syncthreads();
-    int first = i;
-    if (a >= 0) {
-        for (int k = 0; k < i; ++k)
-            if (adp[k] == a) {
-                first = k;
-                break;
-            }
-    }
-    const bool opens = a >= 0 && first == i;
-    const uint32_t b = __ballot_sync(0xffffffffu, opens);
-    if (lane == 0) warp_cnt[warp] = __popc(b);
-    __syncthreads();
-    int before = __popc(b & ((1u << lane) - 1u)), cnt = 0;
-    for (int w = 0; w < 8; ++w) {
-        if (w < warp) before += warp_cnt[w];
-        cnt += warp_cnt[w];
-    }
-    const int64_t base = by_cap ? static_cast<int64_t>(tile) * cap : tile + static_cast<int64_t>(first_q);
-    // a list out of order could ask for more: what does not fit is left out
-    int64_t room = nslots - base;
-    if (room < 0) room = 0;
-    if (room > cap) room = cap;
-    if (opens) slot_at[i] = before < room ? before : -1;
-    if (opens && before < room) slot_adapter[base + before] = a;
-    bad |= cnt > room;
-    __syncthreads();
-    if (i < bn) token_slot[t] = a >= 0 ? slot_at[first] : -1;
-    if (i == 0) {
-        tile_cnt[tile] = static_cast<int32_t>(cnt < room ? cnt : room);
-        tile_base[tile] = static_cast<int32_t>(base < nslots ? base : 0);
-    }
-    if (bad) raise_error(ERRBIT_DEVICE);
-    grid_dep_wait();  // completes after the staging kernel before it, for the GEMM's sake
-}
+constexpr int SHRINK_TOKENS = 32, SHRINK_RANKS = 64, SHRINK_WARPS = 4, SHRINK_THREADS = 32 * SHRINK_WARPS;
+constexpr int SHRINK_PARTS = 8;      // blocks of a cluster
+constexpr int SHRINK_HASH = 512;     // more than twice the tokens of a tile
 
 // eight bf16 of a row from column k on, zero past K
 __device__ __forceinline__ uint4 row8(const uint16_t *__restrict__ row, int64_t k, int64_t K) {
@@ -569,110 +516,246 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// V of one (slot, 32 tokens, 64 ranks): K in blocks of 32, block w, w + 8, ...
-// to warp w; a thread's 16-byte loads of X and A cover the same eight columns,
-// which the two mma k-steps of a block take in a permuted order (the same one
-// for both, so the sum is the product's).  The eight warps' fp32 sums meet in
-// shared memory in a fixed order.  grid: x = 32-token chunks of a tile, y =
-// token tiles, z = rank block + rb x slot lane.
-constexpr int SHRINK_TOKENS = 32, SHRINK_RANKS = 64;
-constexpr int SHRINK_SMEM = 8 * SHRINK_TOKENS * SHRINK_RANKS * 4;
+struct ShrinkArgs {
+    const uint16_t *X, *A;
+    const float *scale;
+    const int32_t *indptr, *ids;
+    int64_t T, K, ldx, lda, sda, nslots;
+    int32_t requests, adapters;
+    int r, rb, bn, cap, by_cap;
+    int32_t *tile_cnt, *tile_base, *slot_adapter;
+    uint16_t *V;
+};
 
-__global__ void __launch_bounds__(256)
-    k_lora_shrink(const uint16_t *__restrict__ X, int64_t T, int64_t K, int64_t ldx,
-                  const uint16_t *__restrict__ A, int64_t lda, int64_t sda, int r, const float *__restrict__ scale,
-                  const int32_t *__restrict__ token_slot, const int32_t *__restrict__ tile_cnt,
-                  const int32_t *__restrict__ tile_base, const int32_t *__restrict__ slot_adapter, int bn, int rb,
-                  uint16_t *__restrict__ V) {
-    extern __shared__ float red[];  // [warp][token][rank]
+struct TilePlan {
+    int32_t start[256], end[256];  // per token of the tile: the request that starts there (its adapter, its end)
+    int32_t slot[256];             // the token's slot, -1: none
+    int32_t adapter[256];          // of a slot
+    int32_t keys[SHRINK_HASH], first[SHRINK_HASH];
+    int32_t warp_max[8], warp_cnt[8];
+    int32_t before, cnt, base;
+};
+
+// Fills in plan.slot, .adapter, .cnt and .base of token tile `tile`; true if the
+// list is out of order or names an unknown adapter (then what it asks for
+// beyond the slots there are is left out).
+__device__ bool plan_tile(const ShrinkArgs &p, int64_t tile, TilePlan &plan) {
+    constexpr int NT = SHRINK_THREADS;
+    const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
+    const int64_t t0 = tile * p.bn, t1 = t0 + p.bn;
+    bool bad = false;
+    for (int k = i; k < 256; k += NT) plan.start[k] = -2;
+    for (int k = i; k < SHRINK_HASH; k += NT) {
+        plan.keys[k] = -1;
+        plan.first[k] = 256;
+    }
+    if (i == 0) plan.before = 0;
+    __syncthreads();
+    int before = 0;
+    for (int32_t q = i; q < p.requests; q += NT) {
+        const int32_t lo = __ldg(p.indptr + q), hi = __ldg(p.indptr + q + 1), a = __ldg(p.ids + q);
+        const bool odd = lo < 0 || lo > hi || hi > p.T || a < -1 || a >= p.adapters;
+        bad |= odd;
+        before += hi <= t0;
+        if (!odd && lo < hi && hi > t0 && lo < t1) {
+            const int at = lo > t0 ? static_cast<int>(lo - t0) : 0;
+            plan.start[at] = a;
+            plan.end[at] = hi;
+        }
+    }
+    if (before) atomicAdd(&plan.before, before);
+    __syncthreads();
+    // the last start at or before each token (two tokens a thread: i and i + 128)
+    int mine[2], a[2], h[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        int m = plan.start[i + u * NT] != -2 ? i + u * NT : -1;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, m, d);
+            if (lane >= d && o > m) m = o;
+        }
+        mine[u] = m;
+        if (lane == 31) plan.warp_max[u * SHRINK_WARPS + warp] = m;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int tok = i + u * NT;
+        for (int w = 0; w < u * SHRINK_WARPS + warp; ++w)
+            if (plan.warp_max[w] > mine[u]) mine[u] = plan.warp_max[w];
+        a[u] = -1;
+        h[u] = 0;
+        if (tok < p.bn && mine[u] >= 0 && t0 + tok < plan.end[mine[u]]) a[u] = plan.start[mine[u]];
+        if (a[u] >= 0) {
+            h[u] = static_cast<int>((static_cast<uint32_t>(a[u]) * 2654435761u) >> 23);
+            while (true) {  // at most 240 keys in 512 places
+                const int32_t old = atomicCAS(&plan.keys[h[u]], -1, a[u]);
+                if (old == -1 || old == a[u]) break;
+                h[u] = (h[u] + 1) & (SHRINK_HASH - 1);
+            }
+            atomicMin(&plan.first[h[u]], tok);
+        }
+    }
+    __syncthreads();
+    uint32_t b[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        b[u] = __ballot_sync(0xffffffffu, a[u] >= 0 && plan.first[h[u]] == i + u * NT);
+        if (lane == 0) plan.warp_cnt[u * SHRINK_WARPS + warp] = __popc(b[u]);
+    }
+    __syncthreads();
+    const int64_t base = p.by_cap ? tile * p.cap : tile + plan.before;
+    int64_t room = p.nslots - base;
+    if (room > p.cap) room = p.cap;
+    if (room < 0) room = 0;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        if ((b[u] >> lane) & 1u) {  // the first token of its adapter: slots in the order of first tokens
+            int at = __popc(b[u] & ((1u << lane) - 1u));
+            for (int w = 0; w < u * SHRINK_WARPS + warp; ++w) at += plan.warp_cnt[w];
+            const bool fits = at < room;
+            bad |= !fits;
+            plan.keys[h[u]] = fits ? at : -1;  // every probe is over: the key's place now holds the slot
+            if (fits) plan.adapter[at] = a[u];
+        }
+    }
+    if (i == 0) {
+        int cnt = 0;
+        for (int w = 0; w < 2 * SHRINK_WARPS; ++w) cnt += plan.warp_cnt[w];
+        plan.cnt = cnt < room ? cnt : static_cast<int>(room);
+        plan.base = base < p.nslots ? static_cast<int32_t>(base) : 0;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 2; ++u) plan.slot[i + u * NT] = a[u] >= 0 ? plan.keys[h[u]] : -1;
+    __syncthreads();
+    return bad;
+}
+
+// NN: 8-rank columns of a block (a rank block has nr / 8 <= NN of them)
+template <int NN>
+__global__ void __launch_bounds__(SHRINK_THREADS)
+    k_lora_shrink(const __grid_constant__ ShrinkArgs p) {
+    constexpr int NR = NN * 8;
+    __shared__ TilePlan plan;
+    __shared__ __align__(16) float red[SHRINK_WARPS][SHRINK_TOKENS][NR];  // [0] holds the block's sums after the first step
     grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tg = lane & 3;
-    const int64_t tile = blockIdx.y, t0 = tile * bn + blockIdx.x * SHRINK_TOKENS;
-    const int in_tile = blockIdx.x * SHRINK_TOKENS;
-    const int rk = static_cast<int>(blockIdx.z % rb) * SHRINK_RANKS;
-    const int lanes_z = gridDim.z / rb;
-    const int nr = r - rk < SHRINK_RANKS ? r - rk : SHRINK_RANKS, nn = nr / 8;
-    grid_dep_wait();
-    const int my = in_tile + lane < bn ? __ldcg(token_slot + t0 + lane) : -1;
-    const int cnt = __ldcg(tile_cnt + tile);
-    const int64_t base = __ldcg(tile_base + tile);
-    for (int j = blockIdx.z / rb; j < cnt; j += lanes_z) {
-        const uint32_t mem = __ballot_sync(0xffffffffu, my == j);  // the same in every warp
-        uint16_t *vrow = V + ((base + j) * bn + in_tile) * static_cast<int64_t>(r) + rk;
-        const int rows = bn - in_tile < SHRINK_TOKENS ? bn - in_tile : SHRINK_TOKENS;
+    const int part = static_cast<int>(cluster_ctarank());
+    const int64_t tile = blockIdx.y;
+    const int in_tile = static_cast<int>(blockIdx.x / SHRINK_PARTS) * SHRINK_TOKENS;
+    const int64_t t0 = tile * p.bn + in_tile;
+    const int rk = static_cast<int>(blockIdx.z % p.rb) * SHRINK_RANKS;
+    const int lanes_z = gridDim.z / p.rb;
+    const int nr = p.r - rk < NR ? p.r - rk : NR, nn = nr / 8;
+    const int rows = p.bn - in_tile < SHRINK_TOKENS ? p.bn - in_tile : SHRINK_TOKENS;
+    const bool bad = plan_tile(p, tile, plan);
+    if (bad) raise_error(ERRBIT_DEVICE);
+    const int cnt = plan.cnt;
+    const int64_t base = plan.base;
+    if (blockIdx.x == 0 && blockIdx.z == 0) {  // what the product reads
+        for (int k = threadIdx.x; k < cnt; k += SHRINK_THREADS) p.slot_adapter[base + k] = plan.adapter[k];
+        if (threadIdx.x == 0) {
+            p.tile_cnt[tile] = cnt;
+            p.tile_base[tile] = static_cast<int32_t>(base);
+        }
+    }
+    const int my = lane < rows ? plan.slot[in_tile + lane] : -1;
+    for (int j = blockIdx.z / p.rb; j < cnt; j += lanes_z) {
+        const uint32_t mem = __ballot_sync(0xffffffffu, my == j);  // the same in every warp and block
+        uint16_t *vrow = p.V + ((base + j) * p.bn + in_tile) * static_cast<int64_t>(p.r) + rk;
         if (mem == 0) {
-            for (int e = threadIdx.x; e < rows * nn; e += 256)
-                *reinterpret_cast<uint4 *>(vrow + static_cast<int64_t>(e / nn) * r + (e % nn) * 8) =
+            for (int e = part * SHRINK_THREADS + threadIdx.x; e < rows * nn; e += SHRINK_PARTS * SHRINK_THREADS)
+                *reinterpret_cast<uint4 *>(vrow + static_cast<int64_t>(e / nn) * p.r + (e % nn) * 8) =
                     make_uint4(0u, 0u, 0u, 0u);
             continue;
         }
-        const int32_t ad = __ldcg(slot_adapter + base + j);
-        const uint16_t *arow = A + ad * sda + static_cast<int64_t>(rk) * lda;
-        float acc[2][8][4];
+        const int32_t ad = plan.adapter[j];
+        const uint16_t *arow = p.A + ad * p.sda + static_cast<int64_t>(rk) * p.lda;
+        float acc[2][NN][4];
 #pragma unroll
-        for (int mtile = 0; mtile < 2; ++mtile)
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-            for (int n = 0; n < 8; ++n)
+            for (int n = 0; n < NN; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[mtile][n][e] = 0.0f;
-        const bool hi = (mem >> 16) != 0u;
-#pragma unroll 2
-        for (int64_t k0 = warp * 32; k0 < K; k0 += 256) {
+                for (int e = 0; e < 4; ++e) acc[mt][n][e] = 0.0f;
+        const bool lo = (mem & 0xFFFFu) != 0u, hi = (mem >> 16) != 0u;
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll NN <= 2 ? 4 : 2
+        for (int64_t k0 = (part * SHRINK_WARPS + warp) * 32; k0 < p.K; k0 += 32 * SHRINK_WARPS * SHRINK_PARTS) {
             const int64_t k = k0 + tg * 8;
-            uint4 x[2][2], b[8];
-            const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+            uint4 x[2][2], b[NN];
 #pragma unroll
-            for (int mtile = 0; mtile < 2; ++mtile)
+            for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const int tok = mtile * 16 + u * 8 + g;
-                    x[mtile][u] = (mem >> tok) & 1u ? row8(X + (t0 + tok) * ldx, k, K) : zero;
+                    const int tok = mt * 16 + u * 8 + g;
+                    x[mt][u] = (mem >> tok) & 1u ? row8(p.X + (t0 + tok) * p.ldx, k, p.K) : zero;
                 }
 #pragma unroll
-            for (int n = 0; n < 8; ++n)
-                b[n] = n < nn ? row8(arow + static_cast<int64_t>(n * 8 + g) * lda, k, K) : zero;
+            for (int n = 0; n < NN; ++n)
+                b[n] = n < nn ? row8(arow + static_cast<int64_t>(n * 8 + g) * p.lda, k, p.K) : zero;
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
+            for (int n = 0; n < NN; ++n) {
                 if (n >= nn) break;
-                mma_16816(acc[0][n], x[0][0].x, x[0][1].x, x[0][0].y, x[0][1].y, b[n].x, b[n].y);
-                mma_16816(acc[0][n], x[0][0].z, x[0][1].z, x[0][0].w, x[0][1].w, b[n].z, b[n].w);
+                if (lo) {
+                    mma_16816(acc[0][n], x[0][0].x, x[0][1].x, x[0][0].y, x[0][1].y, b[n].x, b[n].y);
+                    mma_16816(acc[0][n], x[0][0].z, x[0][1].z, x[0][0].w, x[0][1].w, b[n].z, b[n].w);
+                }
                 if (hi) {
                     mma_16816(acc[1][n], x[1][0].x, x[1][1].x, x[1][0].y, x[1][1].y, b[n].x, b[n].y);
                     mma_16816(acc[1][n], x[1][0].z, x[1][1].z, x[1][0].w, x[1][1].w, b[n].z, b[n].w);
                 }
             }
         }
-        float *mine = red + warp * SHRINK_TOKENS * SHRINK_RANKS;
 #pragma unroll
-        for (int mtile = 0; mtile < 2; ++mtile)
+        for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
+            for (int n = 0; n < NN; ++n) {
                 if (n >= nn) break;
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
-                    *reinterpret_cast<float2 *>(mine + (mtile * 16 + u * 8 + g) * SHRINK_RANKS + n * 8 + 2 * tg) =
-                        make_float2(acc[mtile][n][2 * u], acc[mtile][n][2 * u + 1]);
+                    *reinterpret_cast<float2 *>(&red[warp][mt * 16 + u * 8 + g][n * 8 + 2 * tg]) =
+                        make_float2(acc[mt][n][2 * u], acc[mt][n][2 * u + 1]);
             }
         __syncthreads();
-        const float sc = __ldg(scale + ad);
-        const int half = nr / 2;
-        for (int e = threadIdx.x; e < rows * half; e += 256) {
-            const int tok = e / half, c = 2 * (e % half);
+        for (int e = threadIdx.x; e < SHRINK_TOKENS * nr; e += SHRINK_THREADS) {
+            const int tok = e / nr, c = e % nr;
+            float s = red[0][tok][c];
+#pragma unroll
+            for (int w = 1; w < SHRINK_WARPS; ++w) s += red[w][tok][c];
+            red[0][tok][c] = s;
+        }
+        cluster_sync_all();
+        // block `part` adds four of the 32 tokens over the blocks
+        const float sc = __ldg(p.scale + ad);
+        constexpr int PER = SHRINK_TOKENS / SHRINK_PARTS;
+        for (int e = threadIdx.x; e < PER * nr / 2; e += SHRINK_THREADS) {
+            const int tok = part * PER + e / (nr / 2), c = 2 * (e % (nr / 2));
+            if (tok >= rows) break;
             float s0 = 0.0f, s1 = 0.0f;
             if ((mem >> tok) & 1u) {
+                const uint32_t at = smem_u32(&red[0][tok][c]);
+                float v0[SHRINK_PARTS], v1[SHRINK_PARTS];
 #pragma unroll
-                for (int w = 0; w < 8; ++w) {
-                    const float2 f = *reinterpret_cast<const float2 *>(red + (w * SHRINK_TOKENS + tok) * SHRINK_RANKS + c);
-                    s0 += f.x;
-                    s1 += f.y;
+                for (int w = 0; w < SHRINK_PARTS; ++w) {
+                    uint32_t from;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(at), "r"(w));
+                    v0[w] = ld_dsmem_f32(from);
+                    v1[w] = ld_dsmem_f32(from + 4);
                 }
-                s0 *= sc;
-                s1 *= sc;
+#pragma unroll
+                for (int w = 0; w < SHRINK_PARTS; ++w) {
+                    s0 += v0[w];
+                    s1 += v1[w];
+                }
             }
-            *reinterpret_cast<uint32_t *>(vrow + static_cast<int64_t>(tok) * r + c) = pack_bf16x2(s0, s1);
+            *reinterpret_cast<uint32_t *>(vrow + static_cast<int64_t>(tok) * p.r + c) = pack_bf16x2(s0 * sc, s1 * sc);
         }
-        __syncthreads();
+        cluster_sync_all();  // the sums have been read: the next slot may overwrite them
     }
+    grid_dep_wait();  // completes after the staging kernel before it, for the product's sake
 }
 
 }  // namespace nm
@@ -684,84 +767,108 @@ using namespace nm;
 
 namespace {
 
-// CTA pairs of k_ffn<MODE, OP> that can be resident at once on the current
-// device (0 on a CUDA error), cached per device
+// clusters of 2 * split blocks of k_ffn<MODE, OP> that can be resident at once on
+// the current device (0: none, or a CUDA error), cached per device
 template <int MODE, int OP>
-int64_t ffn_pairs() {
+int64_t ffn_clusters(int split) {
     using Cfg = FfnCfg;
-    static int cache[64] = {};
+    static int cache[64][Cfg::MAX_SPLIT + 1] = {};  // count + 1
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (cache[dev] == 0) {
+    if (cache[dev][split] == 0) {
         if (!set_smem_attr<k_ffn<MODE, OP>>(Cfg::SMEM_BYTES)) return 0;
+        if (split > 4 && cudaFuncSetAttribute(k_ffn<MODE, OP>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+                             cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
         cudaLaunchConfig_t q = {};
-        q.gridDim = dim3(2 * static_cast<unsigned>(sm_count() / 2), 1, 1);
+        q.gridDim = dim3(static_cast<unsigned>(2 * split * (sm_count() / (2 * split))), 1, 1);
         q.blockDim = dim3(Cfg::THREADS, 1, 1);
         q.dynamicSmemBytes = Cfg::SMEM_BYTES;
         cudaLaunchAttribute qa[1];
         qa[0].id = cudaLaunchAttributeClusterDimension;
-        qa[0].val.clusterDim.x = 2;
+        qa[0].val.clusterDim.x = static_cast<unsigned>(2 * split);
         qa[0].val.clusterDim.y = 1;
         qa[0].val.clusterDim.z = 1;
         q.attrs = qa;
         q.numAttrs = 1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, k_ffn<MODE, OP>, &q) != cudaSuccess || n < 1) {
+        if (cudaOccupancyMaxActiveClusters(&n, k_ffn<MODE, OP>, &q) != cudaSuccess) {
             cudaGetLastError();
-            return 0;
+            n = 0;
         }
-        cache[dev] = n < sm_count() / 2 ? n : sm_count() / 2;
+        cache[dev][split] = n + 1;
     }
-    int64_t res = cache[dev];
-    const int forced = g_sched_clusters.load();
-    if (forced > 0 && forced < res) res = forced;
-    if (res > NM_GEMM_STREAMK_MAX_CLUSTERS) res = NM_GEMM_STREAMK_MAX_CLUSTERS;
-    return res < 1 ? 1 : res;
+    return cache[dev][split] - 1;
 }
 
-// tokens per tile: the fewest tiles of at most 240 tokens or, when that is
-// several, one or two more, whichever needs the least (waves over the resident
-// pairs) x (N/2 + 32 clocks an MMA of N tokens costs per K' step)
-int ffn_bn(int64_t T, int64_t n_m, int64_t pairs) {
-    const int64_t nt0 = (T + FfnCfg::BN_MAX - 1) / FfnCfg::BN_MAX;
-    const int64_t nt_last = nt0 >= 2 ? nt0 + 2 : nt0;
-    int64_t best = 0, best_cost = 0;
-    for (int64_t nt = nt0; nt <= nt_last; ++nt) {
-        const int64_t bn = ((T + nt - 1) / nt + 15) / 16 * 16;
-        const int64_t tiles = ((T + bn - 1) / bn) * n_m;
-        const int64_t cost = ((tiles + pairs - 1) / pairs) * (bn + 32);
-        if (best == 0 || cost < best_cost) {
-            best = bn;
-            best_cost = cost;
+// How a call is cut: tokens per tile and pairs per tile.
+struct FfnPlan {
+    int bn, split, stages, sum_off;
+    int64_t clusters;
+};
+
+// The cheapest in SM clocks by this model: rounds of tiles over the resident
+// clusters, each round the K' blocks of a pair (an MMA of N tokens takes N/2 +
+// 32 clocks and there are eight per block; the loads come at some 48 bytes a
+// clock) and a fixed part (epilogue; split: the exchange of the sums).
+template <int MODE, int OP>
+bool ffn_plan(int64_t T, int64_t n_m, int64_t nkb, FfnPlan *best) {
+    using Cfg = FfnCfg;
+    const int forced_split = g_sched_policy.load() == 1 ? 1 : 0;
+    const int forced_clusters = g_sched_clusters.load();
+    const bool must_split = g_sched_policy.load() == 2 && nkb > 1;
+    double best_cost = 0;
+    bool found = false;
+    const int bn_top = static_cast<int>(T < Cfg::BN_MAX ? (T + 15) / 16 * 16 : Cfg::BN_MAX);
+    for (int split = 1; split <= Cfg::MAX_SPLIT && split <= nkb; ++split) {
+        if ((forced_split && split > 1) || (must_split && split == 1)) continue;
+        int64_t clusters = ffn_clusters<MODE, OP>(split);
+        if (forced_clusters > 0 && forced_clusters < clusters) clusters = forced_clusters;
+        if (clusters < 1) continue;
+        for (int bn = bn_top; bn >= 16; bn -= 16) {
+            const int64_t tiles = (T + bn - 1) / bn * n_m, rounds = (tiles + clusters - 1) / clusters;
+            const int sb = Cfg::stage_bytes(bn);
+            int room = Cfg::SMEM_DATA, off = 0;
+            if (split > 1) {  // one round: the sums lie over the idle stages
+                if (Cfg::sum_bytes(bn) > Cfg::SMEM_DATA) continue;
+                if (rounds > 1) room -= Cfg::sum_bytes(bn);
+            }
+            int stages = room / sb;
+            if (stages > Cfg::MAX_STAGES) stages = Cfg::MAX_STAGES;
+            if (stages < 2) continue;
+            if (split > 1 && rounds > 1) off = stages * sb;
+            const double mma = 4.0 * bn + 256, load = sb / 48.0;
+            const double block = mma > load ? mma : load;
+            const double fixed = split > 1 ? 3000 + 24.0 * bn : 1500 + 12.0 * bn;
+            const double cost = rounds * (static_cast<double>((nkb + split - 1) / split) * block + fixed);
+            if (!found || cost < best_cost) {
+                found = true;
+                best_cost = cost;
+                *best = FfnPlan{bn, split, stages, off, tiles < clusters ? tiles : clusters};
+            }
         }
     }
-    return static_cast<int>(best);
+    return found;
 }
 
 template <int MODE, int OP>
-nm_status launch_ffn(const FfnMaps &maps, FfnArgs p, int64_t pairs, void *sk_ws, size_t sk_ws_bytes,
-                     cudaStream_t s) {
+nm_status launch_ffn(const FfnMaps &maps, FfnArgs p, const FfnPlan &plan, cudaStream_t s) {
     using Cfg = FfnCfg;
-    const int64_t Rpad = (p.R + 255) / 256 * 256;
-    const int64_t rows = OP == OP_GLU ? 256 : 512;
-    const int64_t ntiles = ((p.T + p.bn - 1) / p.bn) * ((Rpad + rows - 1) / rows);
-    const int policy = g_sched_policy.load();
-    const bool sk_ok = sk_ws != nullptr && sk_ws_bytes >= ffn_sk_bytes(pairs);
-    const bool sk = sk_ok && (policy == 2 || (policy == 0 && 2 * ntiles <= pairs));
-    const int64_t clusters = sk ? pairs : (ntiles < pairs ? ntiles : pairs);
-    p.stage_bytes = Cfg::stage_bytes(p.bn);
-    p.stages = Cfg::stages(p.bn);
-    p.sk = sk ? 1 : 0;
-    p.sk_ws = sk ? static_cast<uint8_t *>(sk_ws) : nullptr;
-    p.seq = sk ? next_seq() : 0;
+    p.bn = plan.bn;
+    p.split = plan.split;
+    p.stages = plan.stages;
+    p.stage_bytes = Cfg::stage_bytes(plan.bn);
+    p.sum_off = plan.sum_off;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * clusters), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * plan.split * plan.clusters), 1, 1);
     cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
     cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(2 * plan.split);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -769,6 +876,27 @@ nm_status launch_ffn(const FfnMaps &maps, FfnArgs p, int64_t pairs, void *sk_ws,
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, k_ffn<MODE, OP>, maps, p) != cudaSuccess) return NM_ERR_CUDA;
+    return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
+}
+
+template <int NN>
+nm_status launch_shrink(const ShrinkArgs &p, dim3 grid, bool after_staging, cudaStream_t s) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = SHRINK_PARTS;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(SHRINK_THREADS, 1, 1);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    // behind the staging kernel it may start early; else it is the call's first
+    // kernel and follows the stream's earlier work
+    cfg.numAttrs = after_staging ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, k_lora_shrink<NN>, p) != cudaSuccess) return NM_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
 }
 
@@ -818,8 +946,8 @@ nm_status stage_b(const uint16_t *X, int64_t T, int64_t K, int64_t ldx, int m, c
 // bn rows number at most min(requests + tiles, tiles x cap) with cap =
 // min(requests, adapters, bn), bn <= 240 and tiles x bn < T + 240
 struct LoraWs {
-    int64_t token_slot, tiles, slots, v_rows;  // elements of each region
-    size_t o_token, o_cnt, o_base, o_adapter, o_v, bytes;
+    int64_t tiles, slots, v_rows;
+    size_t o_cnt, o_base, o_adapter, o_v, bytes;
 };
 
 LoraWs lora_ws(int64_t T, int64_t r, int64_t requests, int64_t adapters) {
@@ -827,7 +955,6 @@ LoraWs lora_ws(int64_t T, int64_t r, int64_t requests, int64_t adapters) {
     const int64_t bnm = FfnCfg::BN_MAX;
     int64_t cap = requests < adapters ? requests : adapters;
     if (cap > bnm) cap = bnm;
-    l.token_slot = T + bnm;
     l.tiles = T / 16 + 2;
     const int64_t by_req = requests + l.tiles, by_cap = l.tiles * cap;
     l.slots = by_req < by_cap ? by_req : by_cap;
@@ -835,7 +962,6 @@ LoraWs lora_ws(int64_t T, int64_t r, int64_t requests, int64_t adapters) {
     l.v_rows = rows_req < rows_cap ? rows_req : rows_cap;
     auto up = [](size_t b) { return (b + 255) / 256 * 256; };
     size_t o = 0;
-    l.o_token = o, o += up(static_cast<size_t>(l.token_slot) * 4);
     l.o_cnt = o, o += up(static_cast<size_t>(l.tiles) * 4);
     l.o_base = o, o += up(static_cast<size_t>(l.tiles) * 4);
     l.o_adapter = o, o += up(static_cast<size_t>(l.slots) * 4);
@@ -850,7 +976,7 @@ size_t up256(size_t b) { return (b + 255) / 256 * 256; }
 
 extern "C" size_t nm_sparse_glu_workspace_bytes(int64_t T, int64_t K, int m) {
     if (T < 1 || K < 1 || !pattern_ok(m)) return 0;
-    return sk_offset(gemm_ws(T, K, m)) + ffn_sk_bytes(NM_GEMM_STREAMK_MAX_CLUSTERS);
+    return gemm_ws(T, K, m).bytes;
 }
 
 extern "C" nm_status nm_sparse_glu(const uint16_t *X, int64_t T, int64_t K, int64_t ldx, const void *packed_gate,
@@ -869,14 +995,15 @@ extern "C" nm_status nm_sparse_glu(const uint16_t *X, int64_t T, int64_t K, int6
     if (w.bytes > 0 && (!ws || ws_bytes < w.bytes)) return NM_ERR_WORKSPACE;
     const PackedGeom g = packed_geom(R, K, m);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int64_t pairs = m == 8 ? ffn_pairs<PMODE_SP68T, OP_GLU>() : ffn_pairs<PMODE_SP24, OP_GLU>();
-    if (pairs == 0) return NM_ERR_CUDA;
+    FfnPlan plan;
+    if (!(m == 8 ? ffn_plan<PMODE_SP68T, OP_GLU>(T, g.Rpad / 256, g.nkb, &plan)
+                 : ffn_plan<PMODE_SP24, OP_GLU>(T, g.Rpad / 256, g.nkb, &plan)))
+        return NM_ERR_CUDA;
     FfnMaps maps{};
     FfnArgs p{};
     p.T = T;
     p.R = R;
     p.nkb = g.nkb;
-    p.bn = ffn_bn(T, g.Rpad / 256, pairs);
     p.early = m == 8 ? 1 : 0;  // the gather runs just before; X and the weights are older
     p.Y = H;
     p.ldy = ldh;
@@ -886,13 +1013,9 @@ extern "C" nm_status nm_sparse_glu(const uint16_t *X, int64_t T, int64_t K, int6
     p.act = act;
     if (!packed_maps(&maps.a0, &maps.e0, packed_gate, g) || !packed_maps(&maps.a1, &maps.e1, packed_up, g))
         return NM_ERR_CUDA;
-    st = stage_b(X, T, K, ldx, m, g, w, ws, p.bn, &maps, s);
+    st = stage_b(X, T, K, ldx, m, g, w, ws, plan.bn, &maps, s);
     if (st != NM_OK) return st;
-    const size_t sko = sk_offset(w);
-    void *skw = ws && ws_bytes > sko ? static_cast<uint8_t *>(ws) + sko : nullptr;
-    const size_t skb = skw ? ws_bytes - sko : 0;
-    return m == 8 ? launch_ffn<PMODE_SP68T, OP_GLU>(maps, p, pairs, skw, skb, s)
-                  : launch_ffn<PMODE_SP24, OP_GLU>(maps, p, pairs, skw, skb, s);
+    return m == 8 ? launch_ffn<PMODE_SP68T, OP_GLU>(maps, p, plan, s) : launch_ffn<PMODE_SP24, OP_GLU>(maps, p, plan, s);
 }
 
 extern "C" size_t nm_sparse_gemm_lora_workspace_bytes(int64_t T, int64_t K, int m, int64_t r, int64_t adapters,
@@ -900,8 +1023,7 @@ extern "C" size_t nm_sparse_gemm_lora_workspace_bytes(int64_t T, int64_t K, int 
     if (T < 1 || K < 1 || !pattern_ok(m) || r < 8 || r > NM_LORA_MAX_RANK || (r % 8) != 0 || adapters < 1 ||
         requests < 0)
         return 0;
-    return sk_offset(gemm_ws(T, K, m)) + up256(ffn_sk_bytes(NM_GEMM_STREAMK_MAX_CLUSTERS)) +
-           lora_ws(T, r, requests, adapters).bytes;
+    return up256(gemm_ws(T, K, m).bytes) + lora_ws(T, r, requests, adapters).bytes;
 }
 
 extern "C" nm_status nm_sparse_gemm_lora(const uint16_t *X, int64_t T, int64_t K, int64_t ldx, const void *packed,
@@ -928,12 +1050,12 @@ extern "C" nm_status nm_sparse_gemm_lora(const uint16_t *X, int64_t T, int64_t K
     if (l.v_rows > 0x7FFFFFFF || l.slots > 0x7FFFFFFF) return NM_ERR_SHAPE;
     const PackedGeom g = packed_geom(R, K, m);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int64_t pairs = m == 8 ? ffn_pairs<PMODE_SP68T, OP_LORA>() : ffn_pairs<PMODE_SP24, OP_LORA>();
-    if (pairs == 0 || !set_smem_attr<k_lora_shrink>(SHRINK_SMEM)) return NM_ERR_CUDA;
-    uint8_t *skw = static_cast<uint8_t *>(ws) + sk_offset(w);
-    const size_t skb = ffn_sk_bytes(NM_GEMM_STREAMK_MAX_CLUSTERS);
-    uint8_t *lw = skw + up256(skb);
-    int32_t *token_slot = reinterpret_cast<int32_t *>(lw + l.o_token);
+    const int64_t n_m = (g.Rpad + 511) / 512;
+    FfnPlan plan;
+    if (!(m == 8 ? ffn_plan<PMODE_SP68T, OP_LORA>(T, n_m, g.nkb, &plan)
+                 : ffn_plan<PMODE_SP24, OP_LORA>(T, n_m, g.nkb, &plan)))
+        return NM_ERR_CUDA;
+    uint8_t *lw = static_cast<uint8_t *>(ws) + up256(w.bytes);
     int32_t *tile_cnt = reinterpret_cast<int32_t *>(lw + l.o_cnt);
     int32_t *tile_base = reinterpret_cast<int32_t *>(lw + l.o_base);
     int32_t *slot_adapter = reinterpret_cast<int32_t *>(lw + l.o_adapter);
@@ -944,18 +1066,16 @@ extern "C" nm_status nm_sparse_gemm_lora(const uint16_t *X, int64_t T, int64_t K
     p.T = T;
     p.R = R;
     p.nkb = g.nkb;
-    p.bn = ffn_bn(T, (g.Rpad + 511) / 512, pairs);
     p.early = m == 4 || m == 8 ? 1 : 0;  // 4:6 and 8:10 read the lifted activations from the first block on
     p.Y = Y;
     p.ldy = ldy;
     p.rb = static_cast<int>((r + 63) / 64);
-    const int64_t tiles = (T + p.bn - 1) / p.bn;
+    const int64_t tiles = (T + plan.bn - 1) / plan.bn;
     int64_t cap = requests < adapters ? requests : adapters;
-    if (cap > p.bn) cap = p.bn;
-    p.ext_cap = static_cast<int>(cap);
+    if (cap > plan.bn) cap = plan.bn;
     const int by_cap = tiles * cap <= requests + tiles ? 1 : 0;
     const int64_t nslots = by_cap ? tiles * cap : requests + tiles;
-    p.tile_cnt = tile_cnt;
+    p.tile_cnt = cap > 0 ? tile_cnt : nullptr;
     p.tile_base = tile_base;
     p.slot_adapter = slot_adapter;
     if (tiles > 65535) return NM_ERR_SHAPE;
@@ -964,44 +1084,51 @@ extern "C" nm_status nm_sparse_gemm_lora(const uint16_t *X, int64_t T, int64_t K
     maps.e1 = maps.e0;
     if (cap > 0) {
         if (!make_tmap_bf16_3d(&maps.lb, B, adapters, R, r, ldb, sdb, 64, BM) ||
-            !make_tmap_bf16(&maps.lv, V, nslots * p.bn, r, r, 64, static_cast<uint32_t>(p.bn / 2), true))
+            !make_tmap_bf16(&maps.lv, V, nslots * plan.bn, r, r, 64, static_cast<uint32_t>(plan.bn / 2), true))
             return NM_ERR_CUDA;
     } else {
         maps.lb = maps.a0;
         maps.lv = maps.a0;
-        if (m == 4) p.early = 0;  // no kernel of this call runs before the GEMM
+        if (m == 4) p.early = 0;  // no kernel of this call runs before the product
     }
-    st = stage_b(X, T, K, ldx, m, g, w, ws, p.bn, &maps, s);
+    st = stage_b(X, T, K, ldx, m, g, w, ws, plan.bn, &maps, s);
     if (st != NM_OK) return st;
     if (cap > 0) {
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(tiles), 1, 1);
-        cfg.blockDim = dim3(256, 1, 1);
-        cfg.stream = s;
-        cfg.attrs = attr;
-        // behind the staging kernel the plan may start early; else it is this
-        // call's first kernel and follows the stream's earlier work
-        cfg.numAttrs = m == 4 ? 0 : 1;
-        if (cudaLaunchKernelEx(&cfg, k_lora_plan, indptr, ids, static_cast<int32_t>(requests),
-                               static_cast<int32_t>(adapters), T, p.bn, p.ext_cap, by_cap, nslots, token_slot,
-                               tile_cnt, tile_base, slot_adapter) != cudaSuccess)
-            return NM_ERR_CUDA;
-        const int64_t chunks = (p.bn + SHRINK_TOKENS - 1) / SHRINK_TOKENS;
-        int64_t lanes = 2 * sm_count() / (tiles * chunks) + 1;
+        ShrinkArgs a{};
+        a.X = X;
+        a.A = A;
+        a.scale = scale;
+        a.indptr = indptr;
+        a.ids = ids;
+        a.T = T;
+        a.K = K;
+        a.ldx = ldx;
+        a.lda = lda;
+        a.sda = sda;
+        a.nslots = nslots;
+        a.requests = static_cast<int32_t>(requests);
+        a.adapters = static_cast<int32_t>(adapters);
+        a.r = static_cast<int>(r);
+        a.rb = p.rb;
+        a.bn = plan.bn;
+        a.cap = static_cast<int>(cap);
+        a.by_cap = by_cap;
+        a.tile_cnt = tile_cnt;
+        a.tile_base = tile_base;
+        a.slot_adapter = slot_adapter;
+        a.V = V;
+        // slots side by side until the blocks fill the device some four times over
+        const int64_t chunks = (plan.bn + SHRINK_TOKENS - 1) / SHRINK_TOKENS;
+        int64_t lanes = 16 * sm_count() / (tiles * chunks * SHRINK_PARTS) + 1;
         if (lanes > cap) lanes = cap;
-        cfg.gridDim = dim3(static_cast<unsigned>(chunks), static_cast<unsigned>(tiles),
-                           static_cast<unsigned>(lanes * p.rb));
-        cfg.dynamicSmemBytes = SHRINK_SMEM;
-        cfg.numAttrs = 1;
-        if (cudaLaunchKernelEx(&cfg, k_lora_shrink, X, T, K, ldx, A, lda, sda, static_cast<int>(r), scale,
-                               const_cast<const int32_t *>(token_slot), const_cast<const int32_t *>(tile_cnt),
-                               const_cast<const int32_t *>(tile_base), const_cast<const int32_t *>(slot_adapter),
-                               p.bn, p.rb, V) != cudaSuccess)
-            return NM_ERR_CUDA;
+        const dim3 grid(static_cast<unsigned>(SHRINK_PARTS * chunks), static_cast<unsigned>(tiles),
+                        static_cast<unsigned>(lanes * p.rb));
+        st = r <= 8    ? launch_shrink<1>(a, grid, m != 4, s)
+             : r <= 16 ? launch_shrink<2>(a, grid, m != 4, s)
+             : r <= 32 ? launch_shrink<4>(a, grid, m != 4, s)
+                       : launch_shrink<8>(a, grid, m != 4, s);
+        if (st != NM_OK) return st;
     }
-    return m == 8 ? launch_ffn<PMODE_SP68T, OP_LORA>(maps, p, pairs, skw, skb, s)
-                  : launch_ffn<PMODE_SP24, OP_LORA>(maps, p, pairs, skw, skb, s);
+    return m == 8 ? launch_ffn<PMODE_SP68T, OP_LORA>(maps, p, plan, s)
+                  : launch_ffn<PMODE_SP24, OP_LORA>(maps, p, plan, s);
 }
