@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 import threading
 
@@ -105,6 +106,8 @@ class NMError(RuntimeError):
 def load() -> ctypes.CDLL:
     """Load (building first if missing or stale) the CUDA library."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.build()
@@ -435,72 +438,115 @@ def dense_gemm(X, W, Y=None, ws=None, stream=None):
 
 _ACTS = {"silu": 0, "gelu": 1, "relu2": 2}
 
+# The calls below launch kernels of a few microseconds (a decode step), so their
+# checks are written to cost little: no temporary objects, sizes cached.
+
 
 def _act(act):
-    if act not in _ACTS:
+    code = _ACTS.get(act)
+    if code is None:
         raise NMError(f"act must be one of {sorted(_ACTS)}, got {act!r}")
-    return _ACTS[act]
+    return code
 
 
-def _shape(t, name, *shape):
-    if tuple(t.shape) != shape:
+def _shape(t, name, shape):
+    if t.shape != shape:
         raise NMError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    return t
 
 
-def _same_device(**tensors):
-    """Every tensor on one device, and that device the current one: the library
-    launches on the current device."""
-    devs = {t.device for t in tensors.values() if t is not None}
-    if len(devs) > 1:
-        raise NMError(f"{', '.join(tensors)} must be on one device, got {sorted(map(str, devs))}")
-    if devs != {torch.device("cuda", torch.cuda.current_device())}:
-        raise NMError(f"the tensors are on {devs.pop()}, not on the current device")
+def _matrix(t, name, shape):
+    """A bf16 matrix (or stack of matrices) of the given shape."""
+    _bf16(t, name)
+    if t.shape != shape:
+        raise NMError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
 
 
-def _packed(packed, R, K, m, name):
-    _dev(packed, name)
+def _one_device(dev, *tensors):
+    """Every tensor on device `dev`, and that the current one: the library launches
+    on the current device."""
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise NMError(f"all tensors must be on one device, got cuda:{dev} and {t.device}")
+    if dev != torch.cuda.current_device():
+        raise NMError(f"the tensors are on cuda:{dev}, not on the current device")
+
+
+def _scratch(ws, need, X):
+    """(pointer, bytes) of the caller's workspace, or of a new one."""
+    if ws is None:
+        if need == 0:
+            return None, 0, None
+        ws = _out(need, dtype=torch.uint8, device=X.device)
+    return ws.data_ptr(), ws.numel() * ws.element_size(), ws
+
+
+@functools.lru_cache(maxsize=1024)
+def _operand_bytes(R, K, m):
     need = load().nm_sparse_prepare_bytes(R, K, m)
     if need == 0:
         raise NMError(f"unsupported shape or pattern (R={R}, K={K}, m={m})")
-    if not packed.is_contiguous() or packed.numel() * packed.element_size() < need:
+    return need
+
+
+@functools.lru_cache(maxsize=1024)
+def _ws_bytes(name, *sizes):
+    return getattr(load(), name)(*sizes)
+
+
+def _operand(packed, R, K, m, name):
+    _dev(packed, name)
+    if packed.numel() * packed.element_size() < _operand_bytes(R, K, m) or not packed.is_contiguous():
         raise NMError(f"{name} must be a contiguous operand of sparse_prepare(..., R={R}, K={K}, m={m})")
-    return packed
+
+
+_NULL = contextlib.nullcontext()
 
 
 def _on(stream):
     """Context in which outputs and workspaces for a call on `stream` are made: the
     caching allocator then hands their memory on in that stream's order."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _NULL
     return torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
 
 
+def _raw(stream, dev):
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
 def _out_rows(T, R, device):
-    return _out((T, (R + 7) // 8 * 8), dtype=torch.bfloat16, device=device)[:, :R]
+    """bf16 [T x R] with rows on 16 bytes."""
+    ld = (R + 7) // 8 * 8
+    t = _out((T, ld), dtype=torch.bfloat16, device=device)
+    return t if ld == R else t[:, :R]
 
 
 def sparse_glu(X, packed_gate, packed_up, R, m, act="silu", save=False, H=None, ws=None, stream=None):
     """H = act(X Wg^T) * (X Wu^T), both projections sparse, in one kernel; act is
     "silu", "gelu" (tanh form) or "relu2".  save=True returns (H, G, U) with
     G = X Wg^T and U = X Wu^T for sparse_glu_backward."""
-    X = _bf16(X, "X")
+    _bf16(X, "X")
     T, K = X.shape
     a = _act(act)
-    _packed(packed_gate, R, K, m, "packed_gate")
-    _packed(packed_up, R, K, m, "packed_up")
-    _same_device(X=X, packed_gate=packed_gate, packed_up=packed_up, H=H, ws=ws)
-    lib = load()
-    G = U = None
+    _operand(packed_gate, R, K, m, "packed_gate")
+    _operand(packed_up, R, K, m, "packed_up")
+    dev = X.get_device()
+    _one_device(dev, packed_gate, packed_up, H, ws)
+    if H is not None:
+        _matrix(H, "H", (T, R))
+    G = U = g = u = None
+    ld = 0
     with _on(stream):
-        H = _out_rows(T, R, X.device) if H is None else _shape(_bf16(H, "H"), "H", T, R)
+        if H is None:
+            H = _out_rows(T, R, X.device)
         if save:
             G, U = _out_rows(T, R, X.device), _out_rows(T, R, X.device)
-        if ws is None:
-            ws = _out(lib.nm_sparse_glu_workspace_bytes(T, K, m), dtype=torch.uint8, device=X.device)
-    _check(lib.nm_sparse_glu(_ptr(X), T, K, _ld(X), _ptr(packed_gate), _ptr(packed_up), R, m, a, _ptr(H), _ld(H),
-                             _ptr(G), _ptr(U), _ld(G) if save else 0, _ptr(ws), ws.numel() * ws.element_size(),
-                             _stream(stream)), "nm_sparse_glu")
+            g, u, ld = G.data_ptr(), U.data_ptr(), G.stride(0)
+        w, nbytes, ws = _scratch(ws, _ws_bytes("nm_sparse_glu_workspace_bytes", T, K, m), X)
+    st = load().nm_sparse_glu(X.data_ptr(), T, K, X.stride(0), packed_gate.data_ptr(), packed_up.data_ptr(), R, m, a,
+                              H.data_ptr(), H.stride(0), g, u, ld, w, nbytes, _raw(stream, dev))
+    if st:
+        _check(st, "nm_sparse_glu")
     return (H, G, U) if save else H
 
 
@@ -510,54 +556,71 @@ def sparse_glu_backward(dH, X, G, U, Wg, Wu, act="silu", mask_gate=None, mask_up
     Wu are the masked weights in dense form (sparse_densify).  Without masks
     dWg and dWu go straight through to every weight; with the masks of
     prune_compress (pattern width m) they are zero where the mask is."""
-    dH, G, U, Wg, Wu, X = (_bf16(t, n) for t, n in ((dH, "dH"), (G, "G"), (U, "U"), (Wg, "Wg"), (Wu, "Wu"), (X, "X")))
+    _bf16(X, "X")
+    _bf16(Wg, "Wg")
     T, K = X.shape
     R = Wg.shape[0]
     a = _act(act)
-    for t, n, shape in ((dH, "dH", (T, R)), (G, "G", (T, R)), (U, "U", (T, R)), (Wg, "Wg", (R, K)), (Wu, "Wu", (R, K))):
-        _shape(t, n, *shape)
-    if (mask_gate is None) != (mask_up is None) or (mask_gate is not None and m is None):
-        raise NMError("mask_gate, mask_up and m go together")
+    rows, weights = (T, R), (R, K)
+    _matrix(dH, "dH", rows)
+    _matrix(G, "G", rows)
+    _matrix(U, "U", rows)
+    _matrix(Wg, "Wg", weights)
+    _matrix(Wu, "Wu", weights)
     if not need_dx and not need_dw:
         raise NMError("nothing to compute: need_dx and need_dw are both false")
-    if mask_gate is not None:
+    mg = mu = None
+    if mask_gate is not None or mask_up is not None:
+        if mask_gate is None or mask_up is None or m is None:
+            raise NMError("mask_gate, mask_up and m go together")
         for t, n in ((mask_gate, "mask_gate"), (mask_up, "mask_up")):
-            _shape(_dev(t, n), n, R, (n_groups(K, m) * m + 31) // 32)
+            _dev(t, n)
+            _shape(t, n, (R, (n_groups(K, m) * m + 31) // 32))
             if t.element_size() != 4 or not t.is_contiguous():
                 raise NMError(f"{n} must be contiguous 32-bit words")
-    _same_device(dH=dH, X=X, G=G, U=U, Wg=Wg, Wu=Wu, mask_gate=mask_gate, mask_up=mask_up, ws=ws)
-    if _ld(G) != _ld(U) or _ld(Wg) != _ld(Wu):
+        mg, mu = mask_gate.data_ptr(), mask_up.data_ptr()
+    dev = X.get_device()
+    _one_device(dev, dH, G, U, Wg, Wu, mask_gate, mask_up, ws)
+    if G.stride(0) != U.stride(0) or Wg.stride(0) != Wu.stride(0):
         raise NMError("G and U, and Wg and Wu, must have the same row stride")
-    lib = load()
+    dX = dWg = dWu = x = wg = wu = None
+    ldx = ldw = 0
     with _on(stream):
-        dX = _out_rows(T, K, X.device) if need_dx else None
-        dWg, dWu = (_out_rows(R, K, X.device), _out_rows(R, K, X.device)) if need_dw else (None, None)
-        if ws is None:
-            ws = _out(lib.nm_sparse_glu_backward_workspace_bytes(T, R), dtype=torch.uint8, device=X.device)
-    _check(lib.nm_sparse_glu_backward(_ptr(dH), _ld(dH), _ptr(X), T, K, _ld(X), _ptr(G), _ptr(U), _ld(G), _ptr(Wg),
-                                      _ptr(Wu), R, _ld(Wg), a, _ptr(mask_gate), _ptr(mask_up), m or 0, _ptr(dX),
-                                      _ld(dX) if need_dx else 0, _ptr(dWg), _ptr(dWu), _ld(dWg) if need_dw else 0,
-                                      _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
-           "nm_sparse_glu_backward")
+        if need_dx:
+            dX = _out_rows(T, K, X.device)
+            x, ldx = dX.data_ptr(), dX.stride(0)
+        if need_dw:
+            dWg, dWu = _out_rows(R, K, X.device), _out_rows(R, K, X.device)
+            wg, wu, ldw = dWg.data_ptr(), dWu.data_ptr(), dWg.stride(0)
+        w, nbytes, ws = _scratch(ws, _ws_bytes("nm_sparse_glu_backward_workspace_bytes", T, R), X)
+    st = load().nm_sparse_glu_backward(dH.data_ptr(), dH.stride(0), X.data_ptr(), T, K, X.stride(0), G.data_ptr(),
+                                       U.data_ptr(), G.stride(0), Wg.data_ptr(), Wu.data_ptr(), R, Wg.stride(0), a, mg,
+                                       mu, m or 0, x, ldx, wg, wu, ldw, w, nbytes, _raw(stream, dev))
+    if st:
+        _check(st, "nm_sparse_glu_backward")
     return dX, dWg, dWu
 
 
 def sparse_densify(vals, mask, R, K, n, m, W=None, stream=None):
     """mask (.) V in dense form, bf16 [R x K], from prune_compress's kept values
     and mask."""
-    vals = _bf16(vals, "vals")
+    _bf16(vals, "vals")
     _dev(mask, "mask")
     if not 1 <= n < m <= 16:
         raise NMError(f"unsupported pattern {n}:{m}")
-    _shape(vals, "vals", R, n_groups(K, m) * n)
-    _shape(mask, "mask", R, (n_groups(K, m) * m + 31) // 32)
+    _shape(vals, "vals", (R, n_groups(K, m) * n))
+    _shape(mask, "mask", (R, (n_groups(K, m) * m + 31) // 32))
     if not vals.is_contiguous() or not mask.is_contiguous() or mask.element_size() != 4:
         raise NMError("vals and mask must be contiguous, mask of 32-bit words")
-    _same_device(vals=vals, mask=mask, W=W)
-    with _on(stream):
-        W = _out_rows(R, K, vals.device) if W is None else _shape(_bf16(W, "W"), "W", R, K)
-    _check(load().nm_sparse_densify(_ptr(vals), _ptr(mask), R, K, n, m, _ptr(W), _ld(W), _stream(stream)),
-           "nm_sparse_densify")
+    dev = vals.get_device()
+    _one_device(dev, mask, W)
+    if W is not None:
+        _matrix(W, "W", (R, K))
+    else:
+        with _on(stream):
+            W = _out_rows(R, K, vals.device)
+    _check(load().nm_sparse_densify(vals.data_ptr(), mask.data_ptr(), R, K, n, m, W.data_ptr(), W.stride(0),
+                                    _raw(stream, dev)), "nm_sparse_densify")
     return W
 
 
@@ -566,34 +629,40 @@ def sparse_gemm_lora(X, packed, R, m, A, B, scale, indptr, ids, Y=None, ws=None,
     i, scale[a] (X A[a]^T) B[a]^T with a = ids[i] (-1: no adapter).  A
     [adapters x r x K], B [adapters x R x r] bf16, scale fp32 [adapters],
     indptr int32 [requests + 1], ids int32 [requests], all on the device."""
-    X, A, B = _bf16(X, "X"), _bf16(A, "A"), _bf16(B, "B")
+    _bf16(X, "X")
+    _bf16(A, "A")
     T, K = X.shape
-    if A.dim() != 3 or B.dim() != 3:
-        raise NMError("A and B must be [adapters x r x K] and [adapters x R x r]")
-    n, r = A.shape[:2]
-    _shape(A, "A", n, r, K)
-    _shape(B, "B", n, R, r)
-    _packed(packed, R, K, m, "packed")
-    for t, name, dtype in ((scale, "scale", torch.float32), (indptr, "indptr", torch.int32), (ids, "ids", torch.int32)):
-        _dev(t, name)
-        if t.dtype != dtype or t.dim() != 1 or not t.is_contiguous():
-            raise NMError(f"{name} must be a contiguous 1-D tensor of {dtype}")
+    if A.dim() != 3:
+        raise NMError("A must be [adapters x r x K]")
+    n, r, _ = A.shape
+    _shape(A, "A", (n, r, K))
+    _matrix(B, "B", (n, R, r))
+    _operand(packed, R, K, m, "packed")
+    if scale.dtype != torch.float32 or indptr.dtype != torch.int32 or ids.dtype != torch.int32:
+        raise NMError(f"scale must be float32, indptr and ids int32, got {scale.dtype}, {indptr.dtype}, {ids.dtype}")
     q = ids.shape[0]
-    _shape(scale, "scale", n)
-    _shape(indptr, "indptr", q + 1)
-    _same_device(X=X, packed=packed, A=A, B=B, scale=scale, indptr=indptr, ids=ids, Y=Y, ws=ws)
-    lib = load()
-    need = lib.nm_sparse_gemm_lora_workspace_bytes(T, K, m, r, n, q)
+    for t, name, size in ((scale, "scale", n), (indptr, "indptr", q + 1), (ids, "ids", q)):
+        _dev(t, name)
+        _shape(t, name, (size,))
+        if not t.is_contiguous():
+            raise NMError(f"{name} must be contiguous")
+    dev = X.get_device()
+    _one_device(dev, packed, A, B, scale, indptr, ids, Y, ws)
+    need = _ws_bytes("nm_sparse_gemm_lora_workspace_bytes", T, K, m, r, n, q)
     if need == 0:
         raise NMError(f"unsupported adapters (r={r}: a multiple of 8 up to 256; {n} of them)")
+    if Y is not None:
+        _matrix(Y, "Y", (T, R))
     with _on(stream):
-        Y = _out_rows(T, R, X.device) if Y is None else _shape(_bf16(Y, "Y"), "Y", T, R)
-        if ws is None:
-            ws = _out(need, dtype=torch.uint8, device=X.device)
-    _check(lib.nm_sparse_gemm_lora(_ptr(X), T, K, _ld(X), _ptr(packed), R, m, _ptr(A), A.stride(1), A.stride(0),
-                                   _ptr(B), B.stride(1), B.stride(0), _ptr(scale), n, r, _ptr(indptr), _ptr(ids), q,
-                                   _ptr(Y), _ld(Y), _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)),
-           "nm_sparse_gemm_lora")
+        if Y is None:
+            Y = _out_rows(T, R, X.device)
+        w, nbytes, ws = _scratch(ws, need, X)
+    sa, sb = A.stride(), B.stride()
+    st = load().nm_sparse_gemm_lora(X.data_ptr(), T, K, X.stride(0), packed.data_ptr(), R, m, A.data_ptr(), sa[1],
+                                    sa[0], B.data_ptr(), sb[1], sb[0], scale.data_ptr(), n, r, indptr.data_ptr(),
+                                    ids.data_ptr(), q, Y.data_ptr(), Y.stride(0), w, nbytes, _raw(stream, dev))
+    if st:
+        _check(st, "nm_sparse_gemm_lora")
     return Y
 
 

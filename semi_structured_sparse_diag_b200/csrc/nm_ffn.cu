@@ -44,6 +44,7 @@ struct FfnCfg {
     static constexpr int SMEM_BYTES = 232448;
     static constexpr int SMEM_DATA = (SMEM_BYTES - BAR_BYTES - 1024) / 1024 * 1024;
     static constexpr int TMEM_COLS = 512;
+    // accumulator a: columns 256 a ..; its metadata (two buffers of 4 columns) at 240 + 8 a
     static constexpr int TMEM_D0 = 0, TMEM_E0 = 240, TMEM_E1 = 248, TMEM_D1 = 256;
     static_assert(OFF_B % 1024 == 0, "operand alignment");
     static int stage_bytes(int bn) { return OFF_B + bn * 128; }
@@ -65,10 +66,13 @@ struct FfnArgs {
     uint16_t *Y, *G, *U;
     int64_t ldy, ldgu;
     int act;
-    // OP_LORA: adapters per token tile, the tile's first slot, a slot's adapter;
-    // rb blocks of 64 ranks per slot; tile_cnt NULL: no adapters at all
+    // OP_LORA: rows per tile (512, or 256: one accumulator)
+    int tile_rows;
+    // adapters per token tile, the tile's first slot, a slot's adapter; a slot is
+    // rb pieces of `width` ranks, a stage takes 64 / width pieces; tile_cnt NULL:
+    // no adapters at all
     const int32_t *tile_cnt, *tile_base, *slot_adapter;
-    int rb;
+    int rb, width;
 };
 
 __device__ __forceinline__ float act_of(float g, int act) {
@@ -106,22 +110,27 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
     const int64_t cluster = blockIdx.x / (2 * split), nclusters = gridDim.x / (2 * split);
     const int bn = p.bn, bh = bn >> 1;
     const int b_atom = bh * 128;
+    // Narrow tiles keep 2 or 4 partial accumulators of bn columns per
+    // accumulator, one per MMA step in turn: an MMA of few tokens that adds to the
+    // result of the one before it waits for it (about 250 clocks, so a K' block
+    // of 16 tokens took 0.52 us; the loads need 0.37).
+    const int chains = bn <= 48 ? 4 : (bn <= 112 ? 2 : 1);
     const int64_t nkb = p.nkb, T = p.T;
     const int64_t Rpad = (p.R + 255) / 256 * 256;
-    constexpr int TILE_ROWS = OP == OP_GLU ? 256 : 512;
+    const int tile_rows = OP == OP_GLU ? 256 : p.tile_rows;
     const int64_t n_t = (T + bn - 1) / bn;
-    const int64_t n_m = (Rpad + TILE_ROWS - 1) / TILE_ROWS;
+    const int64_t n_m = (Rpad + tile_rows - 1) / tile_rows;
     const int64_t ntiles = n_t * n_m;
     const int64_t kb0 = nkb * part / split, kb1 = nkb * (part + 1) / split;  // this pair's K' blocks
     auto stage = [&](int s) { return smem + s * p.stage_bytes; };
-    // this pair's blocks of the adapters of token tile nt
-    auto adapter_blocks = [&](int64_t nt, int &x0, int &x1) {
-        x0 = x1 = 0;
-        if (OP == OP_LORA && p.tile_cnt != nullptr) {
-            const int n = __ldcg(p.tile_cnt + nt) * p.rb;
-            x0 = n * part / split;
-            x1 = n * (part + 1) / split;
-        }
+    // accumulator 1 in use: rows 256.. of the tile exist
+    auto second = [&](int64_t mt) { return OP == OP_GLU || (tile_rows == 512 && mt * 512 + 256 < Rpad); };
+    // this pair's pieces of the adapters of token tile nt
+    auto adapter_pieces = [&](int64_t nt, int &x0, int &x1) {
+        const int per = 64 / p.width, n = __ldcg(p.tile_cnt + nt) * p.rb, stages = (n + per - 1) / per;
+        x0 = stages * part / split * per;
+        x1 = stages * (part + 1) / split * per;
+        if (x1 > n) x1 = n;
     };
 
     if (threadIdx.x == 0) {
@@ -157,6 +166,8 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
     // that kernel (X, the packed weights) and waits before its first block that
     // is not; the MMA warp reads global memory only for the adapter counts.
     if (warp >= 2 || !p.early) grid_dep_wait();
+    // the stream's next kernel may set itself up on SMs that this one leaves
+    grid_dep_launch();
 
     if (warp == 0) {
         // ---------------------------------------------------------- producer
@@ -173,9 +184,9 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
             };
             for (int64_t tile = cluster; tile < ntiles && ok; tile += nclusters) {
                 int64_t nt, mt;
-                tile_coords(tile, n_t, n_m, BAND_ROWS / TILE_ROWS, nt, mt);
-                const bool has1 = OP == OP_GLU || mt * 512 + 256 < Rpad;
-                const int32_t arow = static_cast<int32_t>(mt * TILE_ROWS + rank * 128);
+                tile_coords(tile, n_t, n_m, BAND_ROWS / tile_rows, nt, mt);
+                const bool has1 = second(mt);
+                const int32_t arow = static_cast<int32_t>(mt * tile_rows + rank * 128);
                 const int32_t arow1 = OP == OP_GLU ? arow : arow + 256;
                 const int32_t brow = static_cast<int32_t>(nt * bn + rank * bh);
                 const int64_t e0 = (arow >> 7) * nkb, e1 = (arow1 >> 7) * nkb;
@@ -211,20 +222,25 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
                         dep_done = true;
                     }
                     int x0, x1;
-                    adapter_blocks(nt, x0, x1);
+                    adapter_pieces(nt, x0, x1);
                     const int32_t slot0 = __ldcg(p.tile_base + nt);
+                    const int per = 64 / p.width, piece = p.width * 2;  // bytes per row of a piece
                     int32_t a_next = x0 < x1 ? __ldcg(p.slot_adapter + slot0 + x0 / p.rb) : 0;
-                    for (int x = x0; x < x1; ++x) {
-                        const int32_t a = a_next, slot = slot0 + x / p.rb, rk = (x % p.rb) * 64;
-                        if (x + 1 < x1) a_next = __ldcg(p.slot_adapter + slot0 + (x + 1) / p.rb);
+                    for (int x = x0; x < x1; x += per) {
                         if (it >= S && !mbar_wait(&empty[s], ph ^ 1u)) { ok = false; break; }
+                        const int n = x1 - x < per ? x1 - x : per;
                         if (rank == 0)
-                            mbar_arrive_expect_tx(&full[s], 2u * ((has1 ? 2u : 1u) * C::A_BYTES + b_bytes / 2));
+                            mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(2 * n * piece * ((has1 ? 2 : 1) * BM + bh)));
                         const uint32_t bar = mapa_shared(&full[s], leader);
                         uint8_t *st = stage(s);
-                        tma_load_3d_pair(st + C::OFF_A0, &tm.lb, bar, rk, arow, a);
-                        if (has1) tma_load_3d_pair(st + C::OFF_A1, &tm.lb, bar, rk, arow + 256, a);
-                        tma_load_2d_pair(st + C::OFF_B, &tm.lv, bar, rk, slot * bn + static_cast<int32_t>(rank) * bh);
+                        for (int k = 0; k < n; ++k) {
+                            const int32_t a = a_next, slot = slot0 + (x + k) / p.rb, rk = ((x + k) % p.rb) * 64;
+                            if (x + k + 1 < x1) a_next = __ldcg(p.slot_adapter + slot0 + (x + k + 1) / p.rb);
+                            tma_load_3d_pair(st + C::OFF_A0 + k * piece * BM, &tm.lb, bar, rk, arow, a);
+                            if (has1) tma_load_3d_pair(st + C::OFF_A1 + k * piece * BM, &tm.lb, bar, rk, arow + 256, a);
+                            tma_load_3d_pair(st + C::OFF_B + k * piece * bh, &tm.lv, bar, rk,
+                                             static_cast<int32_t>(rank) * bh, slot);
+                        }
                         advance();
                     }
                 }
@@ -246,8 +262,8 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
             bool ok = true, dep_done = p.early == 0;
             for (int64_t tile = cluster; tile < ntiles && ok; tile += nclusters, ++ti) {
                 int64_t nt, mt;
-                tile_coords(tile, n_t, n_m, BAND_ROWS / TILE_ROWS, nt, mt);
-                const bool has1 = OP == OP_GLU || mt * 512 + 256 < Rpad;
+                tile_coords(tile, n_t, n_m, BAND_ROWS / tile_rows, nt, mt);
+                const bool has1 = second(mt);
                 if (ti >= 1 && !mbar_wait_cluster(acc_empty, static_cast<uint32_t>((ti - 1) & 1))) break;
                 tc_fence_after();
                 const uint32_t d0 = tmem_base + C::TMEM_D0, d1 = tmem_base + C::TMEM_D1;
@@ -256,18 +272,20 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
                     if (!mbar_wait(&full[s], ph)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t st = smem_u32(stage(s));
-                    tmem_cp_128x128b_pair(te0, make_sdesc(st + C::OFF_E0, 2048, 128, 0));
-                    if (has1) tmem_cp_128x128b_pair(te1, make_sdesc(st + C::OFF_E1, 2048, 128, 0));
+                    const uint32_t eb = static_cast<uint32_t>(kb & 1) * 4u;
+                    tmem_cp_128x128b_pair(te0 + eb, make_sdesc(st + C::OFF_E0, 2048, 128, 0));
+                    if (has1) tmem_cp_128x128b_pair(te1 + eb, make_sdesc(st + C::OFF_E1, 2048, 128, 0));
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const uint64_t bd = make_sdesc(st + C::OFF_B + (j >> 1) * b_atom + (j & 1) * 64, 16, 1024, 2);
-                        const uint32_t acc = (kb > kb0 || j > 0) ? 1u : 0u;
+                        const uint32_t acc = (kb > kb0 || j >= chains) ? 1u : 0u;
                         const uint32_t id = idesc | static_cast<uint32_t>(j & 1);
-                        mma_sp_bf16_pair(d0, make_sdesc(st + C::OFF_A0 + j * 32, 16, 1024, 2), bd,
-                                         te0 + (j & ~1), id, acc);
+                        const uint32_t dc = static_cast<uint32_t>((j & (chains - 1)) * bn);
+                        mma_sp_bf16_pair(d0 + dc, make_sdesc(st + C::OFF_A0 + j * 32, 16, 1024, 2), bd,
+                                         te0 + eb + (j & ~1), id, acc);
                         if (has1)
-                            mma_sp_bf16_pair(d1, make_sdesc(st + C::OFF_A1 + j * 32, 16, 1024, 2), bd,
-                                             te1 + (j & ~1), id, acc);
+                            mma_sp_bf16_pair(d1 + dc, make_sdesc(st + C::OFF_A1 + j * 32, 16, 1024, 2), bd,
+                                             te1 + eb + (j & ~1), id, acc);
                     }
                     mma_commit_pair_mask(&empty[s], both);
                     if (++s == S) { s = 0; ph ^= 1u; }
@@ -278,17 +296,23 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
                         dep_done = true;
                     }
                     int x0, x1;
-                    adapter_blocks(nt, x0, x1);
-                    for (int x = x0; x < x1; ++x) {  // on top of this pair's K' blocks
+                    adapter_pieces(nt, x0, x1);
+                    const int per = 64 / p.width, piece = p.width * 2, steps = p.width / 16;
+                    const uint32_t layout = p.width == 16 ? 6 : (p.width == 32 ? 4 : 2);
+                    for (int x = x0; x < x1; x += per) {  // on top of this pair's K' blocks
                         if (!mbar_wait(&full[s], ph)) { ok = false; break; }
                         tc_fence_after();
                         const uint32_t st = smem_u32(stage(s));
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const uint64_t bd = make_sdesc(st + C::OFF_B + j * 32, 16, 1024, 2);
-                            mma_bf16_pair(d0, make_sdesc(st + C::OFF_A0 + j * 32, 16, 1024, 2), bd, idesc_dense, 1u);
+                        const int n = (x1 - x < per ? x1 - x : per) * steps;
+                        for (int k = 0; k < n; ++k) {  // k-steps of 16 ranks
+                            const int pc = k / steps, in = (k % steps) * 32;
+                            const uint64_t bd = make_sdesc(st + C::OFF_B + pc * piece * bh + in, 16, 8 * piece, layout);
+                            const uint32_t at = st + pc * piece * BM + in;
+                            const uint32_t dc = static_cast<uint32_t>((k & (chains - 1)) * bn);
+                            mma_bf16_pair(d0 + dc, make_sdesc(at + C::OFF_A0, 16, 8 * piece, layout), bd, idesc_dense,
+                                          1u);
                             if (has1)
-                                mma_bf16_pair(d1, make_sdesc(st + C::OFF_A1 + j * 32, 16, 1024, 2), bd, idesc_dense,
+                                mma_bf16_pair(d1 + dc, make_sdesc(at + C::OFF_A1, 16, 8 * piece, layout), bd, idesc_dense,
                                               1u);
                         }
                         mma_commit_pair_mask(&empty[s], both);
@@ -308,7 +332,7 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
         int64_t ti = 0;
         for (int64_t tile = cluster; tile < ntiles; tile += nclusters, ++ti) {
             int64_t nt, mt;
-            tile_coords(tile, n_t, n_m, BAND_ROWS / TILE_ROWS, nt, mt);
+            tile_coords(tile, n_t, n_m, BAND_ROWS / tile_rows, nt, mt);
             if (!__all_sync(0xffffffffu, mbar_wait(acc_full, static_cast<uint32_t>(ti & 1)))) break;
             tc_fence_after();
             const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
@@ -317,7 +341,7 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
             const int nv = static_cast<int>(T - tok0 < bn ? T - tok0 : bn);  // real tokens of the tile
             const int nch = (nv + 15) / 16;                                  // their chunks of 16
             int c_lo = 0, c_hi = nch;
-            const bool active = OP == OP_GLU || h == 0 || mt * 512 + 256 < Rpad;
+            const bool active = h == 0 || second(mt);
             if (OP == OP_GLU) {
                 const int half = (bn / 16 + 1) / 2;
                 c_lo = h ? half : 0;
@@ -325,7 +349,24 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
             } else if (!active) {
                 c_hi = 0;
             }
-            const int64_t row = mt * TILE_ROWS + (OP == OP_LORA ? h * 256 : 0) + rank * 128 + q * 32 + lane;
+            // 16 tokens of the accumulators, the partial ones added up in order
+            auto load_chunk = [&](int c, float (&f)[NACC][16]) {
+#pragma unroll
+                for (int a = 0; a < NACC; ++a) {
+                    uint32_t v[16];
+                    tmem_ld_32x32b_x16(tacc[a] + c * 16, v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) f[a][j] = __uint_as_float(v[j]);
+                    for (int ch = 1; ch < chains; ++ch) {
+                        tmem_ld_32x32b_x16(tacc[a] + ch * bn + c * 16, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) f[a][j] += __uint_as_float(v[j]);
+                    }
+                }
+            };
+            const int64_t row = mt * tile_rows + (OP == OP_LORA ? h * 256 : 0) + rank * 128 + q * 32 + lane;
             const bool rok = row < p.R;
             if (split > 1) {
                 // [accumulator][token][row] fp32 in this CTA's shared memory
@@ -334,15 +375,12 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
                     break;
 #pragma unroll 1
                 for (int c = c_lo; c < c_hi; ++c) {
-                    uint32_t v[NACC][16];
-#pragma unroll
-                    for (int a = 0; a < NACC; ++a) tmem_ld_32x32b_x16(tacc[a] + c * 16, v[a]);
-                    tmem_ld_wait();
+                    float f[NACC][16];
+                    load_chunk(c, f);
 #pragma unroll
                     for (int a = 0; a < NACC; ++a)
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            mine[((OP == OP_GLU ? a : h) * bn + c * 16 + j) * 128] = __uint_as_float(v[a][j]);
+                        for (int j = 0; j < 16; ++j) mine[((OP == OP_GLU ? a : h) * bn + c * 16 + j) * 128] = f[a][j];
                 }
                 tc_fence_before();
                 __syncwarp();
@@ -407,15 +445,8 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
                 for (int k = 0; k < 8; ++k) {
                     const int c = c8 + k;
                     if (c < c_hi) {
-                        uint32_t v[NACC][16];
                         float f[NACC][16];
-#pragma unroll
-                        for (int a = 0; a < NACC; ++a) tmem_ld_32x32b_x16(tacc[a] + c * 16, v[a]);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int a = 0; a < NACC; ++a)
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) f[a][j] = __uint_as_float(v[a][j]);
+                        load_chunk(c, f);
                         if (OP == OP_GLU) {
                             const int64_t t = tok0 + c * 16;
                             if (p.G != nullptr && rok) {
@@ -484,17 +515,19 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
 // each tile or request border starts at most one new pair, so that numbering
 // leaves every tile room and needs requests + tiles slots in all.
 //
-// k_lora_shrink, one (tile, chunk of 32 tokens, rank block of <= 64) per
-// cluster of SHRINK_PARTS blocks that split K.  Every block first works out its
-// tile's slots (one pass over the list, a hash of the adapters; about a
-// microsecond, less than a kernel of its own would take to start), then, for
-// each slot z, z + gridDim.z, ..: the warps run mma.sync over blocks of 32
-// columns; a thread's 16-byte loads of X and A cover the same eight columns,
-// which the two k-steps of a block take in a permuted order (the same one for
-// both operands).  The warps' and then the blocks' fp32 sums are added in a
-// fixed order, through shared and distributed shared memory.
+// k_lora_shrink, one (tile, slot, rank block of <= 64) per cluster of
+// SHRINK_PARTS blocks that split K.  Every block first works out its tile's
+// slots (one pass over the list, a hash of the adapters; about a microsecond,
+// less than a kernel of its own would take to start), then, for its slots,
+// lists the slot's tokens and multiplies 32 of them at a time with mma.sync: a
+// slot of up to 32 tokens has its K split over the warps too, a larger one has
+// groups of 32 tokens side by side in the warps.  A thread's 16-byte loads of X
+// and A cover the same eight columns, which the two k-steps of a block of 32
+// columns take in a permuted order (the same one for both operands), so neither
+// passes through shared memory.  The warps' and then the blocks' fp32 sums are
+// added in a fixed order, through shared and distributed shared memory.
 // ---------------------------------------------------------------------------
-constexpr int SHRINK_TOKENS = 32, SHRINK_RANKS = 64, SHRINK_WARPS = 4, SHRINK_THREADS = 32 * SHRINK_WARPS;
+constexpr int SHRINK_GROUP = 32, SHRINK_RANKS = 64, SHRINK_WARPS = 4, SHRINK_THREADS = 32 * SHRINK_WARPS;
 constexpr int SHRINK_PARTS = 8;      // blocks of a cluster
 constexpr int SHRINK_HASH = 512;     // more than twice the tokens of a tile
 
@@ -523,6 +556,7 @@ struct ShrinkArgs {
     int64_t T, K, ldx, lda, sda, nslots;
     int32_t requests, adapters;
     int r, rb, bn, cap, by_cap;
+    int first;  // the call's first kernel (else it follows the staging kernel)
     int32_t *tile_cnt, *tile_base, *slot_adapter;
     uint16_t *V;
 };
@@ -533,6 +567,7 @@ struct TilePlan {
     int32_t adapter[256];          // of a slot
     int32_t keys[SHRINK_HASH], first[SHRINK_HASH];
     int32_t warp_max[8], warp_cnt[8];
+    int32_t list[256];             // the tokens of the slot at hand
     int32_t before, cnt, base;
 };
 
@@ -639,17 +674,17 @@ __global__ void __launch_bounds__(SHRINK_THREADS)
     k_lora_shrink(const __grid_constant__ ShrinkArgs p) {
     constexpr int NR = NN * 8;
     __shared__ TilePlan plan;
-    __shared__ __align__(16) float red[SHRINK_WARPS][SHRINK_TOKENS][NR];  // [0] holds the block's sums after the first step
+    __shared__ __align__(16) float red[SHRINK_WARPS][SHRINK_GROUP][NR];
+    // as the call's first kernel it waits for the stream's earlier work before it
+    // lets the product start, whose early loads rely on that
+    if (p.first) grid_dep_wait();
     grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tg = lane & 3;
     const int part = static_cast<int>(cluster_ctarank());
-    const int64_t tile = blockIdx.y;
-    const int in_tile = static_cast<int>(blockIdx.x / SHRINK_PARTS) * SHRINK_TOKENS;
-    const int64_t t0 = tile * p.bn + in_tile;
+    const int64_t tile = blockIdx.y, t0 = tile * p.bn;
     const int rk = static_cast<int>(blockIdx.z % p.rb) * SHRINK_RANKS;
     const int lanes_z = gridDim.z / p.rb;
     const int nr = p.r - rk < NR ? p.r - rk : NR, nn = nr / 8;
-    const int rows = p.bn - in_tile < SHRINK_TOKENS ? p.bn - in_tile : SHRINK_TOKENS;
     const bool bad = plan_tile(p, tile, plan);
     if (bad) raise_error(ERRBIT_DEVICE);
     const int cnt = plan.cnt;
@@ -661,83 +696,126 @@ __global__ void __launch_bounds__(SHRINK_THREADS)
             p.tile_base[tile] = static_cast<int32_t>(base);
         }
     }
-    const int my = lane < rows ? plan.slot[in_tile + lane] : -1;
-    for (int j = blockIdx.z / p.rb; j < cnt; j += lanes_z) {
-        const uint32_t mem = __ballot_sync(0xffffffffu, my == j);  // the same in every warp and block
-        uint16_t *vrow = p.V + ((base + j) * p.bn + in_tile) * static_cast<int64_t>(p.r) + rk;
-        if (mem == 0) {
-            for (int e = part * SHRINK_THREADS + threadIdx.x; e < rows * nn; e += SHRINK_PARTS * SHRINK_THREADS)
-                *reinterpret_cast<uint4 *>(vrow + static_cast<int64_t>(e / nn) * p.r + (e % nn) * 8) =
-                    make_uint4(0u, 0u, 0u, 0u);
-            continue;
+    for (int j = blockIdx.z / p.rb; j < cnt; j += lanes_z) {  // the same in every block of the cluster
+        uint16_t *vslot = p.V + (base + j) * p.bn * static_cast<int64_t>(p.r) + rk;
+        // the slot's tokens in ascending order; the other rows are zero
+        uint32_t b[2];
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            b[u] = __ballot_sync(0xffffffffu, plan.slot[threadIdx.x + u * SHRINK_THREADS] == j);
+            if (lane == 0) plan.warp_cnt[u * SHRINK_WARPS + warp] = __popc(b[u]);
         }
+        __syncthreads();
+        int n = 0;
+        for (int w = 0; w < 2 * SHRINK_WARPS; ++w) n += plan.warp_cnt[w];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if ((b[u] >> lane) & 1u) {
+                int at = __popc(b[u] & ((1u << lane) - 1u));
+                for (int w = 0; w < u * SHRINK_WARPS + warp; ++w) at += plan.warp_cnt[w];
+                plan.list[at] = threadIdx.x + u * SHRINK_THREADS;
+            }
+        for (int e = part * SHRINK_THREADS + threadIdx.x; e < p.bn * nn; e += SHRINK_PARTS * SHRINK_THREADS) {
+            const int tok = e / nn;
+            if (plan.slot[tok] != j)
+                *reinterpret_cast<uint4 *>(vslot + static_cast<int64_t>(tok) * p.r + (e - tok * nn) * 8) =
+                    make_uint4(0u, 0u, 0u, 0u);
+        }
+        __syncthreads();
         const int32_t ad = plan.adapter[j];
-        const uint16_t *arow = p.A + ad * p.sda + static_cast<int64_t>(rk) * p.lda;
-        float acc[2][NN][4];
+        const uint16_t *arow = p.A + ad * p.sda + static_cast<int64_t>(rk + g) * p.lda;
+        const float sc = __ldg(p.scale + ad);
+        const bool one = n <= SHRINK_GROUP;  // one group: the warps split K as well
+        for (int first = 0; first < n; first += SHRINK_WARPS * SHRINK_GROUP) {
+            const int g0 = one ? 0 : first + warp * SHRINK_GROUP;   // this warp's group of the list
+            float acc[2][NN][4];
 #pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
+            for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-            for (int n = 0; n < NN; ++n)
+                for (int c = 0; c < NN; ++c)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[mt][n][e] = 0.0f;
-        const bool lo = (mem & 0xFFFFu) != 0u, hi = (mem >> 16) != 0u;
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll NN <= 2 ? 4 : 2
-        for (int64_t k0 = (part * SHRINK_WARPS + warp) * 32; k0 < p.K; k0 += 32 * SHRINK_WARPS * SHRINK_PARTS) {
-            const int64_t k = k0 + tg * 8;
-            uint4 x[2][2], b[NN];
+                    for (int e = 0; e < 4; ++e) acc[mt][c][e] = 0.0f;
+            // rows past the list's end repeat its first token, columns past nr the
+            // first rank: their sums are not read
+            const uint16_t *xr[2][2], *ar[NN];
 #pragma unroll
             for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
-                    const int tok = mt * 16 + u * 8 + g;
-                    x[mt][u] = (mem >> tok) & 1u ? row8(p.X + (t0 + tok) * p.ldx, k, p.K) : zero;
+                    const int at = g0 + mt * 16 + u * 8 + g;
+                    xr[mt][u] = p.X + (t0 + plan.list[at < n ? at : 0]) * p.ldx + tg * 8;
                 }
 #pragma unroll
-            for (int n = 0; n < NN; ++n)
-                b[n] = n < nn ? row8(arow + static_cast<int64_t>(n * 8 + g) * p.lda, k, p.K) : zero;
+            for (int c = 0; c < NN; ++c) ar[c] = arow + static_cast<int64_t>(c < nn ? c * 8 : 0) * p.lda + tg * 8;
+            const bool hi = g0 + 16 < n;  // more than 16 tokens: the second m-tile
+            const int stride = 32 * SHRINK_PARTS * (one ? SHRINK_WARPS : 1);
+            const int K = static_cast<int>(p.K), whole = K & ~31;
+            int k = 32 * (one ? part * SHRINK_WARPS + warp : part);
+            if (g0 >= n) k = K;
+            auto mma = [&](const uint4 (&x)[2][2], const uint4 (&a)[NN]) {
 #pragma unroll
-            for (int n = 0; n < NN; ++n) {
-                if (n >= nn) break;
-                if (lo) {
-                    mma_16816(acc[0][n], x[0][0].x, x[0][1].x, x[0][0].y, x[0][1].y, b[n].x, b[n].y);
-                    mma_16816(acc[0][n], x[0][0].z, x[0][1].z, x[0][0].w, x[0][1].w, b[n].z, b[n].w);
+                for (int c = 0; c < NN; ++c) {
+                    mma_16816(acc[0][c], x[0][0].x, x[0][1].x, x[0][0].y, x[0][1].y, a[c].x, a[c].y);
+                    mma_16816(acc[0][c], x[0][0].z, x[0][1].z, x[0][0].w, x[0][1].w, a[c].z, a[c].w);
+                    if (hi) {
+                        mma_16816(acc[1][c], x[1][0].x, x[1][1].x, x[1][0].y, x[1][1].y, a[c].x, a[c].y);
+                        mma_16816(acc[1][c], x[1][0].z, x[1][1].z, x[1][0].w, x[1][1].w, a[c].z, a[c].w);
+                    }
                 }
-                if (hi) {
-                    mma_16816(acc[1][n], x[1][0].x, x[1][1].x, x[1][0].y, x[1][1].y, b[n].x, b[n].y);
-                    mma_16816(acc[1][n], x[1][0].z, x[1][1].z, x[1][0].w, x[1][1].w, b[n].z, b[n].w);
+            };
+#pragma unroll NN <= 2 ? 4 : 2
+            for (; k < whole; k += stride) {
+                uint4 x[2][2], a[NN];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    x[0][u] = __ldg(reinterpret_cast<const uint4 *>(xr[0][u] + k));
+                    x[1][u] = hi ? __ldg(reinterpret_cast<const uint4 *>(xr[1][u] + k)) : make_uint4(0u, 0u, 0u, 0u);
+                }
+#pragma unroll
+                for (int c = 0; c < NN; ++c) a[c] = __ldg(reinterpret_cast<const uint4 *>(ar[c] + k));
+                mma(x, a);
+            }
+            if (k == whole && k < K) {  // the last, ragged block of columns: one warp's
+                uint4 x[2][2], a[NN];
+                const int64_t left = K - k - tg * 8;
+#pragma unroll
+                for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) x[mt][u] = row8(xr[mt][u] + k, 0, left);
+#pragma unroll
+                for (int c = 0; c < NN; ++c) a[c] = row8(ar[c] + k, 0, left);
+                mma(x, a);
+            }
+#pragma unroll
+            for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+                for (int c = 0; c < NN; ++c) {
+                    if (c >= nn) break;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+                        *reinterpret_cast<float2 *>(&red[warp][mt * 16 + u * 8 + g][c * 8 + 2 * tg]) =
+                            make_float2(acc[mt][c][2 * u], acc[mt][c][2 * u + 1]);
+                }
+            const int groups = one ? 1 : SHRINK_WARPS;
+            if (one) {
+                __syncthreads();
+                for (int e = threadIdx.x; e < n * nr; e += SHRINK_THREADS) {
+                    const int tok = e / nr, c = e - tok * nr;
+                    float s = red[0][tok][c];
+#pragma unroll
+                    for (int w = 1; w < SHRINK_WARPS; ++w) s += red[w][tok][c];
+                    red[0][tok][c] = s;
                 }
             }
-        }
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int n = 0; n < NN; ++n) {
-                if (n >= nn) break;
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-                    *reinterpret_cast<float2 *>(&red[warp][mt * 16 + u * 8 + g][n * 8 + 2 * tg]) =
-                        make_float2(acc[mt][n][2 * u], acc[mt][n][2 * u + 1]);
-            }
-        __syncthreads();
-        for (int e = threadIdx.x; e < SHRINK_TOKENS * nr; e += SHRINK_THREADS) {
-            const int tok = e / nr, c = e % nr;
-            float s = red[0][tok][c];
-#pragma unroll
-            for (int w = 1; w < SHRINK_WARPS; ++w) s += red[w][tok][c];
-            red[0][tok][c] = s;
-        }
-        cluster_sync_all();
-        // block `part` adds four of the 32 tokens over the blocks
-        const float sc = __ldg(p.scale + ad);
-        constexpr int PER = SHRINK_TOKENS / SHRINK_PARTS;
-        for (int e = threadIdx.x; e < PER * nr / 2; e += SHRINK_THREADS) {
-            const int tok = part * PER + e / (nr / 2), c = 2 * (e % (nr / 2));
-            if (tok >= rows) break;
-            float s0 = 0.0f, s1 = 0.0f;
-            if ((mem >> tok) & 1u) {
-                const uint32_t at = smem_u32(&red[0][tok][c]);
-                float v0[SHRINK_PARTS], v1[SHRINK_PARTS];
+            cluster_sync_all();
+            // the round's tokens, one in SHRINK_PARTS to each block, added over the blocks
+            const int left = n - first < groups * SHRINK_GROUP ? n - first : groups * SHRINK_GROUP;
+            const int half = nr / 2;
+            for (int e = threadIdx.x; e < (left + SHRINK_PARTS - 1 - part) / SHRINK_PARTS * half; e += SHRINK_THREADS) {
+                const int i = e / half, c = 2 * (e - i * half), tok = i * SHRINK_PARTS + part;
+                const uint32_t at = smem_u32(&red[0][0][0]) + static_cast<uint32_t>((tok * NR + c) * 4);
+                float v0[SHRINK_PARTS], v1[SHRINK_PARTS], s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
                 for (int w = 0; w < SHRINK_PARTS; ++w) {
                     uint32_t from;
@@ -750,12 +828,13 @@ __global__ void __launch_bounds__(SHRINK_THREADS)
                     s0 += v0[w];
                     s1 += v1[w];
                 }
+                *reinterpret_cast<uint32_t *>(vslot + static_cast<int64_t>(plan.list[first + tok]) * p.r + c) =
+                    pack_bf16x2(s0 * sc, s1 * sc);
             }
-            *reinterpret_cast<uint32_t *>(vrow + static_cast<int64_t>(tok) * p.r + c) = pack_bf16x2(s0 * sc, s1 * sc);
+            cluster_sync_all();  // the sums have been read and may be overwritten
         }
-        cluster_sync_all();  // the sums have been read: the next slot may overwrite them
     }
-    grid_dep_wait();  // completes after the staging kernel before it, for the product's sake
+    if (!p.first) grid_dep_wait();  // completes after the staging kernel, for the product's sake
 }
 
 }  // namespace nm
@@ -805,16 +884,16 @@ int64_t ffn_clusters(int split) {
 
 // How a call is cut: tokens per tile and pairs per tile.
 struct FfnPlan {
-    int bn, split, stages, sum_off;
+    int bn, split, stages, sum_off, tile_rows;
     int64_t clusters;
 };
 
 // The cheapest in SM clocks by this model: rounds of tiles over the resident
 // clusters, each round the K' blocks of a pair (an MMA of N tokens takes N/2 +
-// 32 clocks and there are eight per block; the loads come at some 48 bytes a
-// clock) and a fixed part (epilogue; split: the exchange of the sums).
+// 32 clocks and there are four per accumulator and block; the loads come at some
+// 48 bytes a clock) and a fixed part (epilogue; split: the exchange of the sums).
 template <int MODE, int OP>
-bool ffn_plan(int64_t T, int64_t n_m, int64_t nkb, FfnPlan *best) {
+bool ffn_search(int64_t T, int64_t Rpad, int64_t nkb, FfnPlan *best) {
     using Cfg = FfnCfg;
     const int forced_split = g_sched_policy.load() == 1 ? 1 : 0;
     const int forced_clusters = g_sched_clusters.load();
@@ -827,8 +906,11 @@ bool ffn_plan(int64_t T, int64_t n_m, int64_t nkb, FfnPlan *best) {
         int64_t clusters = ffn_clusters<MODE, OP>(split);
         if (forced_clusters > 0 && forced_clusters < clusters) clusters = forced_clusters;
         if (clusters < 1) continue;
-        for (int bn = bn_top; bn >= 16; bn -= 16) {
-            const int64_t tiles = (T + bn - 1) / bn * n_m, rounds = (tiles + clusters - 1) / clusters;
+        for (int v = 0; v < (OP == OP_LORA ? 2 : 1) * (bn_top / 16); ++v) {
+            const int bn = bn_top - 16 * (v % (bn_top / 16));
+            const int accs = v >= bn_top / 16 ? 1 : 2;  // OP_LORA: 512 rows a tile, or 256
+            const int rows = OP == OP_GLU || accs == 1 ? 256 : 512;
+            const int64_t tiles = (T + bn - 1) / bn * ((Rpad + rows - 1) / rows), rounds = (tiles + clusters - 1) / clusters;
             const int sb = Cfg::stage_bytes(bn);
             int room = Cfg::SMEM_DATA, off = 0;
             if (split > 1) {  // one round: the sums lie over the idle stages
@@ -839,18 +921,43 @@ bool ffn_plan(int64_t T, int64_t n_m, int64_t nkb, FfnPlan *best) {
             if (stages > Cfg::MAX_STAGES) stages = Cfg::MAX_STAGES;
             if (stages < 2) continue;
             if (split > 1 && rounds > 1) off = stages * sb;
-            const double mma = 4.0 * bn + 256, load = sb / 48.0;
+            const double mma = accs * (2.0 * bn + 128);
+            const double load = (sb - (accs == 1 ? Cfg::A_BYTES + EBLK_BYTES : 0)) / 48.0;
             const double block = mma > load ? mma : load;
             const double fixed = split > 1 ? 3000 + 24.0 * bn : 1500 + 12.0 * bn;
             const double cost = rounds * (static_cast<double>((nkb + split - 1) / split) * block + fixed);
             if (!found || cost < best_cost) {
                 found = true;
                 best_cost = cost;
-                *best = FfnPlan{bn, split, stages, off, tiles < clusters ? tiles : clusters};
+                *best = FfnPlan{bn, split, stages, off, rows, tiles < clusters ? tiles : clusters};
             }
         }
     }
     return found;
+}
+
+// the same, looked up: the search takes some 10 us of host time.  It depends on
+// the sizes, the device and the schedule settings only.
+template <int MODE, int OP>
+bool ffn_plan(int64_t T, int64_t Rpad, int64_t nkb, FfnPlan *plan) {
+    struct Entry {
+        int64_t T, Rpad, nkb;
+        int dev, policy, clusters;
+        bool ok;
+        FfnPlan plan;
+    };
+    static thread_local Entry cache[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const int policy = g_sched_policy.load(), clusters = g_sched_clusters.load();
+    Entry &e = cache[static_cast<size_t>((T * 31 + Rpad / 256) * 31 + nkb) % 64];
+    if (!e.ok || e.T != T || e.Rpad != Rpad || e.nkb != nkb || e.dev != dev || e.policy != policy ||
+        e.clusters != clusters) {
+        e = Entry{T, Rpad, nkb, dev, policy, clusters, false, {}};
+        e.ok = ffn_search<MODE, OP>(T, Rpad, nkb, &e.plan);
+    }
+    *plan = e.plan;
+    return e.ok;
 }
 
 template <int MODE, int OP>
@@ -861,6 +968,7 @@ nm_status launch_ffn(const FfnMaps &maps, FfnArgs p, const FfnPlan &plan, cudaSt
     p.stages = plan.stages;
     p.stage_bytes = Cfg::stage_bytes(plan.bn);
     p.sum_off = plan.sum_off;
+    p.tile_rows = plan.tile_rows;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * plan.split * plan.clusters), 1, 1);
     cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
@@ -880,7 +988,7 @@ nm_status launch_ffn(const FfnMaps &maps, FfnArgs p, const FfnPlan &plan, cudaSt
 }
 
 template <int NN>
-nm_status launch_shrink(const ShrinkArgs &p, dim3 grid, bool after_staging, cudaStream_t s) {
+nm_status launch_shrink(const ShrinkArgs &p, dim3 grid, cudaStream_t s) {
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = SHRINK_PARTS;
@@ -893,9 +1001,7 @@ nm_status launch_shrink(const ShrinkArgs &p, dim3 grid, bool after_staging, cuda
     cfg.blockDim = dim3(SHRINK_THREADS, 1, 1);
     cfg.stream = s;
     cfg.attrs = attr;
-    // behind the staging kernel it may start early; else it is the call's first
-    // kernel and follows the stream's earlier work
-    cfg.numAttrs = after_staging ? 2 : 1;
+    cfg.numAttrs = 2;
     if (cudaLaunchKernelEx(&cfg, k_lora_shrink<NN>, p) != cudaSuccess) return NM_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
 }
@@ -996,8 +1102,8 @@ extern "C" nm_status nm_sparse_glu(const uint16_t *X, int64_t T, int64_t K, int6
     const PackedGeom g = packed_geom(R, K, m);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     FfnPlan plan;
-    if (!(m == 8 ? ffn_plan<PMODE_SP68T, OP_GLU>(T, g.Rpad / 256, g.nkb, &plan)
-                 : ffn_plan<PMODE_SP24, OP_GLU>(T, g.Rpad / 256, g.nkb, &plan)))
+    if (!(m == 8 ? ffn_plan<PMODE_SP68T, OP_GLU>(T, g.Rpad, g.nkb, &plan)
+                 : ffn_plan<PMODE_SP24, OP_GLU>(T, g.Rpad, g.nkb, &plan)))
         return NM_ERR_CUDA;
     FfnMaps maps{};
     FfnArgs p{};
@@ -1050,10 +1156,9 @@ extern "C" nm_status nm_sparse_gemm_lora(const uint16_t *X, int64_t T, int64_t K
     if (l.v_rows > 0x7FFFFFFF || l.slots > 0x7FFFFFFF) return NM_ERR_SHAPE;
     const PackedGeom g = packed_geom(R, K, m);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int64_t n_m = (g.Rpad + 511) / 512;
     FfnPlan plan;
-    if (!(m == 8 ? ffn_plan<PMODE_SP68T, OP_LORA>(T, n_m, g.nkb, &plan)
-                 : ffn_plan<PMODE_SP24, OP_LORA>(T, n_m, g.nkb, &plan)))
+    if (!(m == 8 ? ffn_plan<PMODE_SP68T, OP_LORA>(T, g.Rpad, g.nkb, &plan)
+                 : ffn_plan<PMODE_SP24, OP_LORA>(T, g.Rpad, g.nkb, &plan)))
         return NM_ERR_CUDA;
     uint8_t *lw = static_cast<uint8_t *>(ws) + up256(w.bytes);
     int32_t *tile_cnt = reinterpret_cast<int32_t *>(lw + l.o_cnt);
@@ -1069,6 +1174,7 @@ extern "C" nm_status nm_sparse_gemm_lora(const uint16_t *X, int64_t T, int64_t K
     p.early = m == 4 || m == 8 ? 1 : 0;  // 4:6 and 8:10 read the lifted activations from the first block on
     p.Y = Y;
     p.ldy = ldy;
+    p.width = r <= 16 ? 16 : (r <= 32 ? 32 : 64);
     p.rb = static_cast<int>((r + 63) / 64);
     const int64_t tiles = (T + plan.bn - 1) / plan.bn;
     int64_t cap = requests < adapters ? requests : adapters;
@@ -1083,8 +1189,9 @@ extern "C" nm_status nm_sparse_gemm_lora(const uint16_t *X, int64_t T, int64_t K
     maps.a1 = maps.a0;
     maps.e1 = maps.e0;
     if (cap > 0) {
-        if (!make_tmap_bf16_3d(&maps.lb, B, adapters, R, r, ldb, sdb, 64, BM) ||
-            !make_tmap_bf16(&maps.lv, V, nslots * plan.bn, r, r, 64, static_cast<uint32_t>(plan.bn / 2), true))
+        if (!make_tmap_bf16_3d(&maps.lb, B, adapters, R, r, ldb, sdb, static_cast<uint32_t>(p.width), BM) ||
+            !make_tmap_bf16_3d(&maps.lv, V, nslots, plan.bn, r, r, plan.bn * r, static_cast<uint32_t>(p.width),
+                               static_cast<uint32_t>(plan.bn / 2)))
             return NM_ERR_CUDA;
     } else {
         maps.lb = maps.a0;
@@ -1113,20 +1220,20 @@ extern "C" nm_status nm_sparse_gemm_lora(const uint16_t *X, int64_t T, int64_t K
         a.bn = plan.bn;
         a.cap = static_cast<int>(cap);
         a.by_cap = by_cap;
+        a.first = m == 4 ? 1 : 0;
         a.tile_cnt = tile_cnt;
         a.tile_base = tile_base;
         a.slot_adapter = slot_adapter;
         a.V = V;
-        // slots side by side until the blocks fill the device some four times over
-        const int64_t chunks = (plan.bn + SHRINK_TOKENS - 1) / SHRINK_TOKENS;
-        int64_t lanes = 16 * sm_count() / (tiles * chunks * SHRINK_PARTS) + 1;
+        // slots side by side until the blocks fill the device some eight times over
+        int64_t lanes = 8 * sm_count() / (tiles * SHRINK_PARTS) + 1;
         if (lanes > cap) lanes = cap;
-        const dim3 grid(static_cast<unsigned>(SHRINK_PARTS * chunks), static_cast<unsigned>(tiles),
+        const dim3 grid(static_cast<unsigned>(SHRINK_PARTS), static_cast<unsigned>(tiles),
                         static_cast<unsigned>(lanes * p.rb));
-        st = r <= 8    ? launch_shrink<1>(a, grid, m != 4, s)
-             : r <= 16 ? launch_shrink<2>(a, grid, m != 4, s)
-             : r <= 32 ? launch_shrink<4>(a, grid, m != 4, s)
-                       : launch_shrink<8>(a, grid, m != 4, s);
+        st = r <= 8    ? launch_shrink<1>(a, grid, s)
+             : r <= 16 ? launch_shrink<2>(a, grid, s)
+             : r <= 32 ? launch_shrink<4>(a, grid, s)
+                       : launch_shrink<8>(a, grid, s);
         if (st != NM_OK) return st;
     }
     return m == 8 ? launch_ffn<PMODE_SP68T, OP_LORA>(maps, p, plan, s)

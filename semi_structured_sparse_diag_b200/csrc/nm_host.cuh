@@ -53,9 +53,13 @@ inline bool make_tmap_bf16(CUtensorMap *map, const void *base, int64_t rows, int
 }
 
 // 3-D tensor map over `depth` row-major bf16 matrices [rows x cols] (row stride
-// ld, matrix stride sd elements), 128-byte swizzle, boxes of one matrix
+// ld, matrix stride sd elements), boxes of one matrix, box_cols = 16, 32 or 64
+// with the swizzle of that many bytes x 2
 inline bool make_tmap_bf16_3d(CUtensorMap *map, const void *base, int64_t depth, int64_t rows, int64_t cols,
                               int64_t ld, int64_t sd, uint32_t box_cols, uint32_t box_rows) {
+    const CUtensorMapSwizzle swizzle = box_cols == 16   ? CU_TENSOR_MAP_SWIZZLE_32B
+                                       : box_cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                        : CU_TENSOR_MAP_SWIZZLE_128B;
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows),
@@ -64,7 +68,7 @@ inline bool make_tmap_bf16_3d(CUtensorMap *map, const void *base, int64_t depth,
     cuuint32_t box[3] = {box_cols, box_rows, 1};
     cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
