@@ -44,7 +44,6 @@ struct FfnCfg {
     static constexpr int SMEM_BYTES = 232448;
     static constexpr int SMEM_DATA = (SMEM_BYTES - BAR_BYTES - 1024) / 1024 * 1024;
     static constexpr int TMEM_COLS = 512;
-    // accumulator a: columns 256 a ..; its metadata (two buffers of 4 columns) at 240 + 8 a
     static constexpr int TMEM_D0 = 0, TMEM_E0 = 240, TMEM_E1 = 248, TMEM_D1 = 256;
     static_assert(OFF_B % 1024 == 0, "operand alignment");
     static int stage_bytes(int bn) { return OFF_B + bn * 128; }
@@ -110,11 +109,6 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
     const int64_t cluster = blockIdx.x / (2 * split), nclusters = gridDim.x / (2 * split);
     const int bn = p.bn, bh = bn >> 1;
     const int b_atom = bh * 128;
-    // Narrow tiles keep 2 or 4 partial accumulators of bn columns per
-    // accumulator, one per MMA step in turn: an MMA of few tokens that adds to the
-    // result of the one before it waits for it (about 250 clocks, so a K' block
-    // of 16 tokens took 0.52 us; the loads need 0.37).
-    const int chains = bn <= 48 ? 4 : (bn <= 112 ? 2 : 1);
     const int64_t nkb = p.nkb, T = p.T;
     const int64_t Rpad = (p.R + 255) / 256 * 256;
     const int tile_rows = OP == OP_GLU ? 256 : p.tile_rows;
@@ -252,10 +246,22 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA issuer
-        if (rank == 0 && lane == 0) {
+        // The whole warp runs the loop and one elected lane issues, on operand
+        // descriptors that differ from those of stage 0 by one addition: with
+        // N = 16 the tensor core waits for the issuing thread, not for data.
+        if (rank == 0) {
+            const bool lead = elect_one() != 0u;
             const uint32_t idesc = make_idesc_bf16(256, bn, true, 0);
-            const uint32_t idesc_dense = make_idesc_bf16(256, bn, false, 0);
             const uint16_t both = static_cast<uint16_t>(3u << leader);
+            const uint32_t st0 = smem_u32(smem);
+            const uint64_t a0d = make_sdesc(st0 + C::OFF_A0, 16, 1024, 2), a1d = make_sdesc(st0 + C::OFF_A1, 16, 1024, 2);
+            const uint64_t b0d = make_sdesc(st0 + C::OFF_B, 16, 1024, 2);
+            const uint64_t b1d = make_sdesc(st0 + C::OFF_B + b_atom, 16, 1024, 2);
+            const uint64_t e0d = make_sdesc(st0 + C::OFF_E0, 2048, 128, 0), e1d = make_sdesc(st0 + C::OFF_E1, 2048, 128, 0);
+            const uint32_t step = static_cast<uint32_t>(p.stage_bytes) >> 4;
+            const uint32_t d0 = tmem_base + C::TMEM_D0, d1 = tmem_base + C::TMEM_D1;
+            const uint32_t te0 = tmem_base + C::TMEM_E0, te1 = tmem_base + C::TMEM_E1;
+            const int nblocks = static_cast<int>(kb1 - kb0);
             int s = 0;
             uint32_t ph = 0;
             int64_t ti = 0;
@@ -266,28 +272,24 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
                 const bool has1 = second(mt);
                 if (ti >= 1 && !mbar_wait_cluster(acc_empty, static_cast<uint32_t>((ti - 1) & 1))) break;
                 tc_fence_after();
-                const uint32_t d0 = tmem_base + C::TMEM_D0, d1 = tmem_base + C::TMEM_D1;
-                const uint32_t te0 = tmem_base + C::TMEM_E0, te1 = tmem_base + C::TMEM_E1;
-                for (int64_t kb = kb0; kb < kb1; ++kb) {
+                for (int kb = 0; kb < nblocks; ++kb) {
                     if (!mbar_wait(&full[s], ph)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t st = smem_u32(stage(s));
-                    const uint32_t eb = static_cast<uint32_t>(kb & 1) * 4u;
-                    tmem_cp_128x128b_pair(te0 + eb, make_sdesc(st + C::OFF_E0, 2048, 128, 0));
-                    if (has1) tmem_cp_128x128b_pair(te1 + eb, make_sdesc(st + C::OFF_E1, 2048, 128, 0));
+                    const uint64_t so = static_cast<uint64_t>(static_cast<uint32_t>(s) * step);
+                    if (lead) {
+                        tmem_cp_128x128b_pair(te0, e0d + so);
+                        if (has1) tmem_cp_128x128b_pair(te1, e1d + so);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint64_t bd = make_sdesc(st + C::OFF_B + (j >> 1) * b_atom + (j & 1) * 64, 16, 1024, 2);
-                        const uint32_t acc = (kb > kb0 || j >= chains) ? 1u : 0u;
-                        const uint32_t id = idesc | static_cast<uint32_t>(j & 1);
-                        const uint32_t dc = static_cast<uint32_t>((j & (chains - 1)) * bn);
-                        mma_sp_bf16_pair(d0 + dc, make_sdesc(st + C::OFF_A0 + j * 32, 16, 1024, 2), bd,
-                                         te0 + eb + (j & ~1), id, acc);
-                        if (has1)
-                            mma_sp_bf16_pair(d1 + dc, make_sdesc(st + C::OFF_A1 + j * 32, 16, 1024, 2), bd,
-                                             te1 + eb + (j & ~1), id, acc);
+                        for (int j = 0; j < 4; ++j) {
+                            const uint64_t bd = (j >> 1 ? b1d : b0d) + so + (j & 1) * 4;
+                            const uint32_t acc = j > 0 || kb > 0 ? 1u : 0u;
+                            const uint32_t id = idesc | static_cast<uint32_t>(j & 1);
+                            mma_sp_bf16_pair(d0, a0d + so + j * 2, bd, te0 + (j & ~1), id, acc);
+                            if (has1) mma_sp_bf16_pair(d1, a1d + so + j * 2, bd, te1 + (j & ~1), id, acc);
+                        }
+                        mma_commit_pair_mask(&empty[s], both);
                     }
-                    mma_commit_pair_mask(&empty[s], both);
+                    __syncwarp();
                     if (++s == S) { s = 0; ph ^= 1u; }
                 }
                 if (OP == OP_LORA && ok && p.tile_cnt != nullptr) {
@@ -297,29 +299,32 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
                     }
                     int x0, x1;
                     adapter_pieces(nt, x0, x1);
+                    const uint32_t idesc_dense = make_idesc_bf16(256, bn, false, 0);
                     const int per = 64 / p.width, piece = p.width * 2, steps = p.width / 16;
                     const uint32_t layout = p.width == 16 ? 6 : (p.width == 32 ? 4 : 2);
                     for (int x = x0; x < x1; x += per) {  // on top of this pair's K' blocks
                         if (!mbar_wait(&full[s], ph)) { ok = false; break; }
                         tc_fence_after();
-                        const uint32_t st = smem_u32(stage(s));
-                        const int n = (x1 - x < per ? x1 - x : per) * steps;
-                        for (int k = 0; k < n; ++k) {  // k-steps of 16 ranks
-                            const int pc = k / steps, in = (k % steps) * 32;
-                            const uint64_t bd = make_sdesc(st + C::OFF_B + pc * piece * bh + in, 16, 8 * piece, layout);
-                            const uint32_t at = st + pc * piece * BM + in;
-                            const uint32_t dc = static_cast<uint32_t>((k & (chains - 1)) * bn);
-                            mma_bf16_pair(d0 + dc, make_sdesc(at + C::OFF_A0, 16, 8 * piece, layout), bd, idesc_dense,
-                                          1u);
-                            if (has1)
-                                mma_bf16_pair(d1 + dc, make_sdesc(at + C::OFF_A1, 16, 8 * piece, layout), bd, idesc_dense,
-                                              1u);
+                        if (lead) {
+                            const uint32_t st = st0 + static_cast<uint32_t>(s) * p.stage_bytes;
+                            const int n = (x1 - x < per ? x1 - x : per) * steps;
+                            for (int k = 0; k < n; ++k) {  // k-steps of 16 ranks
+                                const int pc = k / steps, in = (k % steps) * 32;
+                                const uint64_t bd = make_sdesc(st + C::OFF_B + pc * piece * bh + in, 16, 8 * piece, layout);
+                                const uint32_t at = st + pc * piece * BM + in;
+                                mma_bf16_pair(d0, make_sdesc(at + C::OFF_A0, 16, 8 * piece, layout), bd, idesc_dense, 1u);
+                                if (has1)
+                                    mma_bf16_pair(d1, make_sdesc(at + C::OFF_A1, 16, 8 * piece, layout), bd, idesc_dense,
+                                                  1u);
+                            }
+                            mma_commit_pair_mask(&empty[s], both);
                         }
-                        mma_commit_pair_mask(&empty[s], both);
+                        __syncwarp();
                         if (++s == S) { s = 0; ph ^= 1u; }
                     }
                 }
-                if (ok) mma_commit_pair_mask(acc_full, both);
+                if (ok && lead) mma_commit_pair_mask(acc_full, both);
+                __syncwarp();
             }
         }
     } else if (warp >= 4 && warp < 12) {
@@ -349,22 +354,16 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
             } else if (!active) {
                 c_hi = 0;
             }
-            // 16 tokens of the accumulators, the partial ones added up in order
+            // 16 tokens of the accumulators
             auto load_chunk = [&](int c, float (&f)[NACC][16]) {
+                uint32_t v[NACC][16];
 #pragma unroll
-                for (int a = 0; a < NACC; ++a) {
-                    uint32_t v[16];
-                    tmem_ld_32x32b_x16(tacc[a] + c * 16, v);
-                    tmem_ld_wait();
+                for (int a = 0; a < NACC; ++a) tmem_ld_32x32b_x16(tacc[a] + c * 16, v[a]);
+                tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) f[a][j] = __uint_as_float(v[j]);
-                    for (int ch = 1; ch < chains; ++ch) {
-                        tmem_ld_32x32b_x16(tacc[a] + ch * bn + c * 16, v);
-                        tmem_ld_wait();
+                for (int a = 0; a < NACC; ++a)
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) f[a][j] += __uint_as_float(v[j]);
-                    }
-                }
+                    for (int j = 0; j < 16; ++j) f[a][j] = __uint_as_float(v[a][j]);
             };
             const int64_t row = mt * tile_rows + (OP == OP_LORA ? h * 256 : 0) + rank * 128 + q * 32 + lane;
             const bool rok = row < p.R;
