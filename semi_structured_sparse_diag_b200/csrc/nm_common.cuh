@@ -406,12 +406,22 @@ __device__ __forceinline__ void tma_load_2d_pair(void *smem_dst, const void *tma
         : "memory");
 }
 
-// the same from a stack of matrices (3-D tensor map): matrix z
-__device__ __forceinline__ void tma_load_3d_pair(void *smem_dst, const void *tmap, uint32_t bar_cluster,
-                                                 int32_t x, int32_t y, int32_t z) {
+// the same with the destination given as a shared-memory address, and from a
+// stack of matrices (3-D tensor map): matrix z
+__device__ __forceinline__ void tma_load_2d_pair_at(uint32_t dst, const void *tmap, uint32_t bar_cluster, int32_t x,
+                                                    int32_t y) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar_cluster), "r"(x), "r"(y)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_pair_at(uint32_t dst, const void *tmap, uint32_t bar_cluster, int32_t x,
+                                                    int32_t y, int32_t z) {
     asm volatile(
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
+        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar_cluster), "r"(x), "r"(y), "r"(z)
         : "memory");
 }

@@ -165,84 +165,86 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
 
     if (warp == 0) {
         // ---------------------------------------------------------- producer
-        if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 0;
-            int64_t it = 0;
-            bool ok = true, dep_done = p.early == 0;
-            const uint32_t b_bytes = 2u * static_cast<uint32_t>(b_atom);
-            const CUtensorMap *ta1 = OP == OP_GLU ? &tm.a1 : &tm.a0, *te1 = OP == OP_GLU ? &tm.e1 : &tm.e0;
-            auto advance = [&]() {
-                ++it;
-                if (++s == S) { s = 0; ph ^= 1u; }
-            };
-            for (int64_t tile = cluster; tile < ntiles && ok; tile += nclusters) {
-                int64_t nt, mt;
-                tile_coords(tile, n_t, n_m, BAND_ROWS / tile_rows, nt, mt);
-                const bool has1 = second(mt);
-                const int32_t arow = static_cast<int32_t>(mt * tile_rows + rank * 128);
-                const int32_t arow1 = OP == OP_GLU ? arow : arow + 256;
-                const int32_t brow = static_cast<int32_t>(nt * bn + rank * bh);
-                const int64_t e0 = (arow >> 7) * nkb, e1 = (arow1 >> 7) * nkb;
-                const uint32_t tx = 2u * ((has1 ? 2u : 1u) * (C::A_BYTES + EBLK_BYTES) + b_bytes);
-                for (int64_t v = kb0; v < kb1; ++v) {
-                    const int64_t kb = MODE == PMODE_SP68T ? visit68(v, nkb) : v;
-                    const bool mid = MODE == PMODE_SP68T && (kb % 3) == 2;
-                    if (mid && !dep_done) {  // written by the kernel just before
-                        grid_dep_wait();
-                        dep_done = true;
-                    }
-                    if (it >= S && !mbar_wait(&empty[s], ph ^ 1u)) { ok = false; break; }
+        // (the warp in step, one lane issues: as below)
+        const bool lead = elect_one() != 0u;
+        const uint32_t st0 = smem_u32(smem), full0 = mapa_shared(full, leader);
+        const uint32_t b_bytes = 2u * static_cast<uint32_t>(b_atom);
+        const CUtensorMap *ta1 = OP == OP_GLU ? &tm.a1 : &tm.a0, *te1 = OP == OP_GLU ? &tm.e1 : &tm.e0;
+        const int nraw = 2 * static_cast<int>(nkb / 3);
+        int s = 0;
+        uint32_t ph = 0;
+        int64_t it = 0;
+        bool ok = true, dep_done = p.early == 0;
+        for (int64_t tile = cluster; tile < ntiles && ok; tile += nclusters) {
+            int64_t nt, mt;
+            tile_coords(tile, n_t, n_m, BAND_ROWS / tile_rows, nt, mt);
+            const bool has1 = second(mt);
+            const int32_t arow = static_cast<int32_t>(mt * tile_rows + rank * 128);
+            const int32_t arow1 = OP == OP_GLU ? arow : arow + 256;
+            const int32_t brow = static_cast<int32_t>(nt * bn + rank * bh);
+            const int32_t e0 = static_cast<int32_t>((arow >> 7) * nkb * 8), e1 = static_cast<int32_t>((arow1 >> 7) * nkb * 8);
+            const uint32_t tx = 2u * ((has1 ? 2u : 1u) * (C::A_BYTES + EBLK_BYTES) + b_bytes);
+            for (int v = static_cast<int>(kb0); v < static_cast<int>(kb1); ++v, ++it) {
+                // 6:8: tiles of X first, the gathered middle windows last (visit68)
+                const bool mid = MODE == PMODE_SP68T && v >= nraw;
+                const int kb = MODE != PMODE_SP68T ? v : (mid ? 3 * (v - nraw) + 2 : 3 * (v >> 1) + (v & 1));
+                const int xc = MODE != PMODE_SP68T ? v * 128 : (mid ? v - nraw : v) * 128;
+                if (mid && !dep_done) {  // written by the kernel just before
+                    grid_dep_wait();
+                    dep_done = true;
+                }
+                if (it >= S && !mbar_wait(&empty[s], ph ^ 1u)) { ok = false; break; }
+                if (lead) {
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], tx);
-                    const uint32_t bar = mapa_shared(&full[s], leader);
-                    uint8_t *st = stage(s);
-                    const int32_t ka = static_cast<int32_t>(kb * 64);
-                    tma_load_2d_pair(st + C::OFF_A0, &tm.a0, bar, ka, arow);
-                    tma_load_2d_pair(st + C::OFF_E0, &tm.e0, bar, 0, static_cast<int32_t>((e0 + kb) * 8));
-                    if (has1) {
-                        tma_load_2d_pair(st + C::OFF_A1, ta1, bar, ka, arow1);
-                        tma_load_2d_pair(st + C::OFF_E1, te1, bar, 0, static_cast<int32_t>((e1 + kb) * 8));
-                    }
-                    const int64_t xc = MODE == PMODE_SP24 ? kb * 128
-                                       : (mid ? (kb / 3) * 128 : (kb / 3) * 256 + (kb % 3) * 128);
+                    const uint32_t bar = full0 + static_cast<uint32_t>(s) * 8u;
+                    const uint32_t st = st0 + static_cast<uint32_t>(s) * p.stage_bytes;
+                    tma_load_2d_pair_at(st + C::OFF_A0, &tm.a0, bar, kb * 64, arow);
+                    if (has1) tma_load_2d_pair_at(st + C::OFF_A1, ta1, bar, kb * 64, arow1);
                     const CUtensorMap *tb = mid ? &tm.b2 : &tm.b;
-                    tma_load_2d_pair(st + C::OFF_B, tb, bar, static_cast<int32_t>(xc), brow);
-                    tma_load_2d_pair(st + C::OFF_B + b_atom, tb, bar, static_cast<int32_t>(xc + 64), brow);
-                    advance();
+                    tma_load_2d_pair_at(st + C::OFF_B, tb, bar, xc, brow);
+                    tma_load_2d_pair_at(st + C::OFF_B + b_atom, tb, bar, xc + 64, brow);
+                    tma_load_2d_pair_at(st + C::OFF_E0, &tm.e0, bar, 0, e0 + kb * 8);
+                    if (has1) tma_load_2d_pair_at(st + C::OFF_E1, te1, bar, 0, e1 + kb * 8);
                 }
-                if (OP == OP_LORA && ok && p.tile_cnt != nullptr) {
-                    if (!dep_done) {
-                        grid_dep_wait();
-                        dep_done = true;
-                    }
-                    int x0, x1;
-                    adapter_pieces(nt, x0, x1);
-                    const int32_t slot0 = __ldcg(p.tile_base + nt);
-                    const int per = 64 / p.width, piece = p.width * 2;  // bytes per row of a piece
-                    int32_t a_next = x0 < x1 ? __ldcg(p.slot_adapter + slot0 + x0 / p.rb) : 0;
-                    for (int x = x0; x < x1; x += per) {
-                        if (it >= S && !mbar_wait(&empty[s], ph ^ 1u)) { ok = false; break; }
-                        const int n = x1 - x < per ? x1 - x : per;
-                        if (rank == 0)
-                            mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(2 * n * piece * ((has1 ? 2 : 1) * BM + bh)));
-                        const uint32_t bar = mapa_shared(&full[s], leader);
-                        uint8_t *st = stage(s);
-                        for (int k = 0; k < n; ++k) {
-                            const int32_t a = a_next, slot = slot0 + (x + k) / p.rb, rk = ((x + k) % p.rb) * 64;
-                            if (x + k + 1 < x1) a_next = __ldcg(p.slot_adapter + slot0 + (x + k + 1) / p.rb);
-                            tma_load_3d_pair(st + C::OFF_A0 + k * piece * BM, &tm.lb, bar, rk, arow, a);
-                            if (has1) tma_load_3d_pair(st + C::OFF_A1 + k * piece * BM, &tm.lb, bar, rk, arow + 256, a);
-                            tma_load_3d_pair(st + C::OFF_B + k * piece * bh, &tm.lv, bar, rk,
-                                             static_cast<int32_t>(rank) * bh, slot);
+                __syncwarp();
+                if (++s == S) { s = 0; ph ^= 1u; }
+            }
+            if (OP == OP_LORA && ok && p.tile_cnt != nullptr) {
+                if (!dep_done) {
+                    grid_dep_wait();
+                    dep_done = true;
+                }
+                int x0, x1;
+                adapter_pieces(nt, x0, x1);
+                const int32_t slot0 = __ldcg(p.tile_base + nt);
+                const int per = 64 / p.width, piece = p.width * 2;  // bytes per row of a piece
+                int32_t a_next = x0 < x1 ? __ldcg(p.slot_adapter + slot0 + x0 / p.rb) : 0;
+                for (int x = x0; x < x1; x += per, ++it) {
+                    if (it >= S && !mbar_wait(&empty[s], ph ^ 1u)) { ok = false; break; }
+                    const int n = x1 - x < per ? x1 - x : per;
+                    const uint32_t bar = full0 + static_cast<uint32_t>(s) * 8u;
+                    const uint32_t st = st0 + static_cast<uint32_t>(s) * p.stage_bytes;
+                    if (lead && rank == 0)
+                        mbar_arrive_expect_tx(&full[s], static_cast<uint32_t>(2 * n * piece * ((has1 ? 2 : 1) * BM + bh)));
+                    for (int k = 0; k < n; ++k) {
+                        const int32_t a = a_next, slot = slot0 + (x + k) / p.rb, rk = ((x + k) % p.rb) * 64;
+                        if (x + k + 1 < x1) a_next = __ldcg(p.slot_adapter + slot0 + (x + k + 1) / p.rb);
+                        if (lead) {
+                            tma_load_3d_pair_at(st + C::OFF_A0 + k * piece * BM, &tm.lb, bar, rk, arow, a);
+                            if (has1)
+                                tma_load_3d_pair_at(st + C::OFF_A1 + k * piece * BM, &tm.lb, bar, rk, arow + 256, a);
+                            tma_load_3d_pair_at(st + C::OFF_B + k * piece * bh, &tm.lv, bar, rk,
+                                                static_cast<int32_t>(rank) * bh, slot);
                         }
-                        advance();
                     }
+                    __syncwarp();
+                    if (++s == S) { s = 0; ph ^= 1u; }
                 }
             }
-            if (!ok && rank == 0) {  // let copies already issued land before exiting
-                for (int64_t j = (it > S ? it - S : 0); j < it; ++j)
-                    mbar_wait(&full[j % S], static_cast<uint32_t>((j / S) & 1));
-            }
+        }
+        if (!ok && rank == 0) {  // let copies already issued land before exiting
+            for (int64_t j = (it > S ? it - S : 0); j < it; ++j)
+                mbar_wait(&full[j % S], static_cast<uint32_t>((j / S) & 1));
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA issuer
