@@ -89,7 +89,10 @@ __device__ __forceinline__ float act_of(float g, int act) {
 // shared memory in the pairs' order (so results do not depend on timing), and
 // finishes those tokens.  Nothing goes through global memory and nothing
 // outlives the launch.
-template <int MODE, int OP>
+// (SPLIT is a template parameter because the exchange's registers would spill
+// in the plain epilogue, which held up the next tile: 850 -> 1390 us for the
+// gate and up projections of 8192 tokens.)
+template <int MODE, int OP, bool SPLIT>
 __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
     k_ffn(const __grid_constant__ FfnMaps tm, const __grid_constant__ FfnArgs p) {
     using C = FfnCfg;
@@ -105,7 +108,7 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t crank = cluster_ctarank(), rank = crank & 1u, leader = crank & ~1u;
-    const int split = p.split, part = static_cast<int>(crank >> 1);
+    const int split = SPLIT ? p.split : 1, part = SPLIT ? static_cast<int>(crank >> 1) : 0;
     const int64_t cluster = blockIdx.x / (2 * split), nclusters = gridDim.x / (2 * split);
     const int bn = p.bn, bh = bn >> 1;
     const int b_atom = bh * 128;
@@ -331,10 +334,12 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
         }
     } else if (warp >= 4 && warp < 12) {
         // ---------------------------------------------------------- epilogue
-        // OP_GLU : warp = lane quarter q x token half h, both accumulators
-        // OP_LORA: warp = lane quarter q x accumulator h, all tokens
+        // a warp = lane quarter q x half h: of the tokens where one warp needs both
+        // accumulators (OP_GLU) or there is but one (256 rows a tile), else h is
+        // the accumulator
         const int q = warp & 3, h = (warp - 4) >> 2;
         constexpr int NACC = OP == OP_GLU ? 2 : 1;
+        const bool by_tokens = OP == OP_GLU || tile_rows == 256;
         const uint32_t acc_empty_cl = mapa_shared(acc_empty, leader);
         int64_t ti = 0;
         for (int64_t tile = cluster; tile < ntiles; tile += nclusters, ++ti) {
@@ -343,13 +348,14 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
             if (!__all_sync(0xffffffffu, mbar_wait(acc_full, static_cast<uint32_t>(ti & 1)))) break;
             tc_fence_after();
             const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-            const uint32_t tacc[2] = {tq + (OP == OP_LORA && h ? C::TMEM_D1 : C::TMEM_D0), tq + C::TMEM_D1};
+            const int acc0 = by_tokens ? 0 : h;  // the (first) accumulator of this warp
+            const uint32_t tacc[2] = {tq + (acc0 ? C::TMEM_D1 : C::TMEM_D0), tq + C::TMEM_D1};
             const int64_t tok0 = nt * bn;
             const int nv = static_cast<int>(T - tok0 < bn ? T - tok0 : bn);  // real tokens of the tile
             const int nch = (nv + 15) / 16;                                  // their chunks of 16
             int c_lo = 0, c_hi = nch;
-            const bool active = h == 0 || second(mt);
-            if (OP == OP_GLU) {
+            const bool active = acc0 == 0 || second(mt);
+            if (by_tokens) {
                 const int half = (bn / 16 + 1) / 2;
                 c_lo = h ? half : 0;
                 c_hi = h ? nch : (nch < half ? nch : half);
@@ -367,11 +373,11 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) f[a][j] = __uint_as_float(v[a][j]);
             };
-            const int64_t row = mt * tile_rows + (OP == OP_LORA ? h * 256 : 0) + rank * 128 + q * 32 + lane;
+            const int64_t row = mt * tile_rows + acc0 * 256 + rank * 128 + q * 32 + lane;
             const bool rok = row < p.R;
-            if (split > 1) {
-                // [accumulator][token][row] fp32 in this CTA's shared memory
-                float *mine = reinterpret_cast<float *>(smem + p.sum_off) + q * 32 + lane;
+            if constexpr (SPLIT) {
+                // this CTA's sums in its shared memory: [accumulator][4 tokens][row][token], fp32
+                float4 *mine = reinterpret_cast<float4 *>(smem + p.sum_off) + acc0 * (bn / 4) * 128 + q * 32 + lane;
                 if (ti >= 1 && !__all_sync(0xffffffffu, mbar_wait_cluster(sum_free, static_cast<uint32_t>((ti - 1) & 1))))
                     break;
 #pragma unroll 1
@@ -381,56 +387,73 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
 #pragma unroll
                     for (int a = 0; a < NACC; ++a)
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) mine[((OP == OP_GLU ? a : h) * bn + c * 16 + j) * 128] = f[a][j];
+                        for (int j = 0; j < 4; ++j)
+                            mine[(a * (bn / 4) + c * 4 + j) * 128] =
+                                make_float4(f[a][4 * j], f[a][4 * j + 1], f[a][4 * j + 2], f[a][4 * j + 3]);
                 }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(acc_empty_cl);
                 if (lane < split) mbar_arrive_cluster(mapa_shared(sum_ready, 2 * lane + rank));
                 if (!__all_sync(0xffffffffu, mbar_wait_cluster(sum_ready, static_cast<uint32_t>(ti & 1)))) break;
-                // this pair's tokens, every second one to each half of the warps
-                // (OP_GLU) or all of them to each accumulator's (OP_LORA)
-                constexpr int STEP = OP == OP_GLU ? 2 : 1;
-                const int t1 = active ? nv * (part + 1) / split : 0;
+                // this pair's share of the tokens, four at a time; all the parts of
+                // GROUPS x 4 tokens are in flight before the first is used
+                constexpr int GROUPS = OP == OP_GLU ? 1 : 2;
+                const int ng = (nv + 3) / 4, g1 = active ? ng * (part + 1) / split : 0;
+                const int gstep = by_tokens ? 2 : 1;
                 const uint32_t off = smem_u32(mine);
                 uint32_t from[C::MAX_SPLIT];
 #pragma unroll
-                for (int i = 0; i < C::MAX_SPLIT; ++i) {
+                for (int i = 0; i < C::MAX_SPLIT; ++i)
                     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
                                  : "=r"(from[i]) : "r"(off), "r"(2 * (i < split ? i : part) + rank));
-                }
 #pragma unroll 1
-                for (int t = nv * part / split + (OP == OP_GLU ? h : 0); t < t1; t += 2 * STEP) {
-                    float f[NACC][2];
+                for (int g = ng * part / split + (by_tokens ? h : 0); g < g1; g += gstep * GROUPS) {
+                    float4 pv[C::MAX_SPLIT][GROUPS][NACC];
 #pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int tt = t + u * STEP < t1 ? t + u * STEP : t;
+                    for (int i = 0; i < C::MAX_SPLIT; ++i)
+                        if (i < split) {
+#pragma unroll
+                            for (int u = 0; u < GROUPS; ++u)
+#pragma unroll
+                                for (int a = 0; a < NACC; ++a) {
+                                    const int gg = g + u * gstep < g1 ? g + u * gstep : g;
+                                    pv[i][u][a] = ld_dsmem_f32x4(from[i] + static_cast<uint32_t>((a * (bn / 4) + gg) * 2048));
+                                }
+                        }
+#pragma unroll
+                    for (int u = 0; u < GROUPS; ++u) {
+                        if (g + u * gstep >= g1) break;
+                        float f[NACC][4];
 #pragma unroll
                         for (int a = 0; a < NACC; ++a) {
-                            const uint32_t at = static_cast<uint32_t>(((OP == OP_GLU ? a : h) * bn + tt) * 512);
-                            float pv[C::MAX_SPLIT];
-#pragma unroll
-                            for (int i = 0; i < C::MAX_SPLIT; ++i)
-                                pv[i] = i < split ? ld_dsmem_f32(from[i] + at) : 0.0f;
-                            f[a][u] = pv[0];
+                            f[a][0] = pv[0][u][a].x;
+                            f[a][1] = pv[0][u][a].y;
+                            f[a][2] = pv[0][u][a].z;
+                            f[a][3] = pv[0][u][a].w;
 #pragma unroll
                             for (int i = 1; i < C::MAX_SPLIT; ++i)
-                                if (i < split) f[a][u] += pv[i];
-                        }
-                    }
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const int64_t tk = tok0 + t + u * STEP;
-                        if (t + u * STEP < t1 && rok) {
-                            if (OP == OP_GLU) {
-                                if (p.G != nullptr) {
-                                    p.G[tk * p.ldgu + row] = static_cast<uint16_t>(pack_bf16x2(f[0][u], 0.0f));
-                                    p.U[tk * p.ldgu + row] = static_cast<uint16_t>(pack_bf16x2(f[NACC - 1][u], 0.0f));
+                                if (i < split) {
+                                    f[a][0] += pv[i][u][a].x;
+                                    f[a][1] += pv[i][u][a].y;
+                                    f[a][2] += pv[i][u][a].z;
+                                    f[a][3] += pv[i][u][a].w;
                                 }
-                                f[0][u] = act_of(f[0][u], p.act) * f[NACC - 1][u];
-                            }
-                            p.Y[tk * p.ldy + row] = static_cast<uint16_t>(pack_bf16x2(f[0][u], 0.0f));
                         }
+                        const int t = (g + u * gstep) * 4;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            if (t + j < nv && rok) {
+                                const int64_t tk = tok0 + t + j;
+                                if (OP == OP_GLU) {
+                                    if (p.G != nullptr) {
+                                        p.G[tk * p.ldgu + row] = static_cast<uint16_t>(pack_bf16x2(f[0][j], 0.0f));
+                                        p.U[tk * p.ldgu + row] = static_cast<uint16_t>(pack_bf16x2(f[NACC - 1][j], 0.0f));
+                                    }
+                                    f[0][j] = act_of(f[0][j], p.act) * f[NACC - 1][j];
+                                }
+                                p.Y[tk * p.ldy + row] = static_cast<uint16_t>(pack_bf16x2(f[0][j], 0.0f));
+                            }
                     }
                 }
                 __syncwarp();
@@ -847,17 +870,17 @@ using namespace nm;
 
 namespace {
 
-// clusters of 2 * split blocks of k_ffn<MODE, OP> that can be resident at once on
+// clusters of 2 * split blocks of a k_ffn that can be resident at once on
 // the current device (0: none, or a CUDA error), cached per device
-template <int MODE, int OP>
-int64_t ffn_clusters(int split) {
+template <auto kernel>
+int64_t ffn_clusters_of(int split) {
     using Cfg = FfnCfg;
     static int cache[64][Cfg::MAX_SPLIT + 1] = {};  // count + 1
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
     if (cache[dev][split] == 0) {
-        if (!set_smem_attr<k_ffn<MODE, OP>>(Cfg::SMEM_BYTES)) return 0;
-        if (split > 4 && cudaFuncSetAttribute(k_ffn<MODE, OP>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+        if (!set_smem_attr<kernel>(Cfg::SMEM_BYTES)) return 0;
+        if (split > 4 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
                              cudaSuccess) {
             cudaGetLastError();
             return 0;
@@ -874,13 +897,18 @@ int64_t ffn_clusters(int split) {
         q.attrs = qa;
         q.numAttrs = 1;
         int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, k_ffn<MODE, OP>, &q) != cudaSuccess) {
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &q) != cudaSuccess) {
             cudaGetLastError();
             n = 0;
         }
         cache[dev][split] = n + 1;
     }
     return cache[dev][split] - 1;
+}
+
+template <int MODE, int OP>
+int64_t ffn_clusters(int split) {
+    return split > 1 ? ffn_clusters_of<k_ffn<MODE, OP, true>>(split) : ffn_clusters_of<k_ffn<MODE, OP, false>>(1);
 }
 
 // How a call is cut: tokens per tile and pairs per tile.
@@ -892,7 +920,8 @@ struct FfnPlan {
 // The cheapest in SM clocks by this model: rounds of tiles over the resident
 // clusters, each round the K' blocks of a pair (an MMA of N tokens takes N/2 +
 // 32 clocks and there are four per accumulator and block; the loads come at some
-// 48 bytes a clock) and a fixed part (epilogue; split: the exchange of the sums).
+// 64 bytes a clock) and a fixed part: the epilogue, or with a split the exchange
+// of the sums, 512 bytes per token and accumulator at some 18 bytes a clock.
 template <int MODE, int OP>
 bool ffn_search(int64_t T, int64_t Rpad, int64_t nkb, FfnPlan *best) {
     using Cfg = FfnCfg;
@@ -923,9 +952,9 @@ bool ffn_search(int64_t T, int64_t Rpad, int64_t nkb, FfnPlan *best) {
             if (stages < 2) continue;
             if (split > 1 && rounds > 1) off = stages * sb;
             const double mma = accs * (2.0 * bn + 128);
-            const double load = (sb - (accs == 1 ? Cfg::A_BYTES + EBLK_BYTES : 0)) / 48.0;
+            const double load = (sb - (accs == 1 ? Cfg::A_BYTES + EBLK_BYTES : 0)) / 64.0;
             const double block = mma > load ? mma : load;
-            const double fixed = split > 1 ? 3000 + 24.0 * bn : 1500 + 12.0 * bn;
+            const double fixed = split > 1 ? 3000 + accs * 28.0 * bn : 1500 + 12.0 * bn;
             const double cost = rounds * (static_cast<double>((nkb + split - 1) / split) * block + fixed);
             if (!found || cost < best_cost) {
                 found = true;
@@ -984,7 +1013,9 @@ nm_status launch_ffn(const FfnMaps &maps, FfnArgs p, const FfnPlan &plan, cudaSt
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, k_ffn<MODE, OP>, maps, p) != cudaSuccess) return NM_ERR_CUDA;
+    const cudaError_t e = plan.split > 1 ? cudaLaunchKernelEx(&cfg, k_ffn<MODE, OP, true>, maps, p)
+                                         : cudaLaunchKernelEx(&cfg, k_ffn<MODE, OP, false>, maps, p);
+    if (e != cudaSuccess) return NM_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
 }
 
