@@ -517,8 +517,9 @@ def _raw(stream, dev):
 def _out_rows(T, R, device):
     """bf16 [T x R] with rows on 16 bytes."""
     ld = (R + 7) // 8 * 8
-    t = _out((T, ld), dtype=torch.bfloat16, device=device)
-    return t if ld == R else t[:, :R]
+    if _POISON:
+        return _out((T, ld), dtype=torch.bfloat16, device=device)[:, :R]
+    return torch.empty_strided((T, R), (ld, 1), dtype=torch.bfloat16, device=device)
 
 
 def sparse_glu(X, packed_gate, packed_up, R, m, act="silu", save=False, H=None, ws=None, stream=None):

@@ -458,60 +458,61 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
                 }
                 __syncwarp();
                 if (lane < split) mbar_arrive_cluster(mapa_shared(sum_free, 2 * lane + rank));
-                continue;
             }
-            uint32_t pk[8][8];
-            // two passes of eight chunks (OP_GLU: one); the accumulator is released
-            // once the last chunk is in registers, before its stores
+            if constexpr (!SPLIT) {
+                uint32_t pk[8][8];
+                // two passes of eight chunks (OP_GLU: one); the accumulator is released
+                // once the last chunk is in registers, before its stores
 #pragma unroll 1
-            for (int c8 = c_lo; c8 < c_hi || c8 == c_lo; c8 += 8) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int c = c8 + k;
-                    if (c < c_hi) {
-                        float f[NACC][16];
-                        load_chunk(c, f);
-                        if (OP == OP_GLU) {
-                            const int64_t t = tok0 + c * 16;
-                            if (p.G != nullptr && rok) {
-                                uint16_t *gp = p.G + t * p.ldgu + row, *up = p.U + t * p.ldgu + row;
-#pragma unroll
-                                for (int j = 0; j < 16; j += 2) {
-                                    const uint32_t g2 = pack_bf16x2(f[0][j], f[0][j + 1]);
-                                    const uint32_t u2 = pack_bf16x2(f[NACC - 1][j], f[NACC - 1][j + 1]);
-                                    if (c * 16 + j < nv) {
-                                        gp[j * p.ldgu] = static_cast<uint16_t>(g2 & 0xFFFFu);
-                                        up[j * p.ldgu] = static_cast<uint16_t>(u2 & 0xFFFFu);
-                                    }
-                                    if (c * 16 + j + 1 < nv) {
-                                        gp[(j + 1) * p.ldgu] = static_cast<uint16_t>(g2 >> 16);
-                                        up[(j + 1) * p.ldgu] = static_cast<uint16_t>(u2 >> 16);
-                                    }
-                                }
-                            }
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) f[0][j] = act_of(f[0][j], p.act) * f[NACC - 1][j];
-                        }
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) pk[k][i] = pack_bf16x2(f[0][2 * i], f[0][2 * i + 1]);
-                    }
-                }
-                if (c8 + 8 >= c_hi) {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(acc_empty_cl);
-                }
-                if (rok) {
+                for (int c8 = c_lo; c8 < c_hi || c8 == c_lo; c8 += 8) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         const int c = c8 + k;
                         if (c < c_hi) {
-                            uint16_t *yp = p.Y + (tok0 + c * 16) * p.ldy + row;
+                            float f[NACC][16];
+                            load_chunk(c, f);
+                            if (OP == OP_GLU) {
+                                const int64_t t = tok0 + c * 16;
+                                if (p.G != nullptr && rok) {
+                                    uint16_t *gp = p.G + t * p.ldgu + row, *up = p.U + t * p.ldgu + row;
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                if (c * 16 + 2 * i < nv) yp[0] = static_cast<uint16_t>(pk[k][i] & 0xFFFFu);
-                                if (c * 16 + 2 * i + 1 < nv) yp[p.ldy] = static_cast<uint16_t>(pk[k][i] >> 16);
-                                yp += 2 * p.ldy;
+                                    for (int j = 0; j < 16; j += 2) {
+                                        const uint32_t g2 = pack_bf16x2(f[0][j], f[0][j + 1]);
+                                        const uint32_t u2 = pack_bf16x2(f[NACC - 1][j], f[NACC - 1][j + 1]);
+                                        if (c * 16 + j < nv) {
+                                            gp[j * p.ldgu] = static_cast<uint16_t>(g2 & 0xFFFFu);
+                                            up[j * p.ldgu] = static_cast<uint16_t>(u2 & 0xFFFFu);
+                                        }
+                                        if (c * 16 + j + 1 < nv) {
+                                            gp[(j + 1) * p.ldgu] = static_cast<uint16_t>(g2 >> 16);
+                                            up[(j + 1) * p.ldgu] = static_cast<uint16_t>(u2 >> 16);
+                                        }
+                                    }
+                                }
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) f[0][j] = act_of(f[0][j], p.act) * f[NACC - 1][j];
+                            }
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) pk[k][i] = pack_bf16x2(f[0][2 * i], f[0][2 * i + 1]);
+                        }
+                    }
+                    if (c8 + 8 >= c_hi) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(acc_empty_cl);
+                    }
+                    if (rok) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) {
+                            const int c = c8 + k;
+                            if (c < c_hi) {
+                                uint16_t *yp = p.Y + (tok0 + c * 16) * p.ldy + row;
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    if (c * 16 + 2 * i < nv) yp[0] = static_cast<uint16_t>(pk[k][i] & 0xFFFFu);
+                                    if (c * 16 + 2 * i + 1 < nv) yp[p.ldy] = static_cast<uint16_t>(pk[k][i] >> 16);
+                                    yp += 2 * p.ldy;
+                                }
                             }
                         }
                     }

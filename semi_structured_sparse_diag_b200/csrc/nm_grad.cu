@@ -93,44 +93,102 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------------------
-// C[M x N] = sum over the contraction of A and B, dense bf16 operands, fp32
-// accumulation, bf16 C.  Persistent CTA pairs, 256 x 256 tiles, two
-// accumulators in tensor memory (the epilogue of a tile overlaps the next
-// tile's MMAs), six 32 KB stages; warps as in k_gemm_pair.
-//   GRAD_X : A = dG, then dU [T x R] (K-major), B = Wg, then Wu [R x K]
-//            (MN-major); the contraction is R twice.  C = dX [T x K].
-//   GRAD_W : A = dG or dU [T x R], B = X [T x K], both MN-major, contraction T.
-//            Two problems side by side: tiles of dWg, then of dWu.
+// The three products in one launch: dense bf16 operands, fp32 accumulation,
+// bf16 results.  Persistent CTA pairs, 256 x 256 tiles, two accumulators in
+// tensor memory (the epilogue of a tile overlaps the next tile's MMAs), six
+// 32 KB stages; warps as in k_gemm_pair, with the loading and the issuing warp
+// in step and one lane of each at work.
+//   dX  [T x K]: A = dG, then dU [T x R] (K-major), B = Wg, then Wu [R x K]
+//       (MN-major); the contraction is R twice.
+//   dWg, dWu [R x K]: A = dG or dU [T x R], B = X [T x K], both MN-major,
+//       contraction T.
 // MN-major operand tiles: TMA boxes of 64 columns x 64 contraction rows
 // (128-byte swizzle): rows of 128 bytes are consecutive contraction steps, so
 // eight of them make a swizzle atom (1024 bytes, the descriptor's stride
 // offset) and the next 64 columns lie one box (8192 bytes, the leading
 // offset) further; a k-step of 16 advances by two atoms.
+//
+// The tiles of dX come first, then those of dWg and dWu.  With few tokens dX
+// has too few tiles for the device and a long contraction (and reads all of Wg
+// and Wu): a cluster of `split` pairs then shares one tile of it, each with its
+// part of the contraction, and the fp32 sums are added through distributed
+// shared memory, in the pairs' order, as in the gated product (SPLIT).
 // ---------------------------------------------------------------------------
-enum { GRAD_X = 0, GRAD_W = 1 };
-
 struct GradCfg {
     static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGES = 6;
+    static constexpr int MAX_SPLIT = 8;
+    static constexpr int SUM_BYTES = 256 * 128 * 4;        // a CTA's sums, over the idle stages
     static constexpr int EPI_WARPS = 8;
     static constexpr int EPI_BYTES = EPI_WARPS * 32 * 128;  // 32 rows x 64 columns bf16 each
     static constexpr int THREADS = 384;
     static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + EPI_BYTES + 256 + 1024;
-    static_assert(SMEM_BYTES <= 232448, "shared memory");
+    static_assert(SMEM_BYTES <= 232448 && SUM_BYTES <= STAGES * STAGE_BYTES, "shared memory");
 };
 
 struct GradMaps {
-    CUtensorMap a[2], b[2], c[2];
+    CUtensorMap g[2];              // dG, dU as dX's A (boxes 64 x 128)
+    CUtensorMap w[2];              // Wg, Wu (boxes 64 x 64)
+    CUtensorMap gt[2], x;          // dG, dU and X as operands of dW (boxes 64 x 64)
+    CUtensorMap dx, dw[2];         // the results
 };
 
 struct GradArgs {
-    int64_t M, N, nkb;             // rows, columns; contraction blocks of 64 of one source
-    const uint32_t *mask[2];       // GRAD_W: keep bits of C's columns (or NULL: all kept)
-    int64_t mask_words;            // words per row
+    int64_t T, R, K;
+    int64_t tiles_x, tiles_w;      // tiles of dX; of dWg (and of dWu)
+    int split;
+    uint16_t *dX;
+    int64_t lddx;
+    const uint32_t *mask[2];       // keep bits of dWg, dWu (or NULL: all kept)
+    int64_t mask_words;            // per row
 };
 
-template <int KIND>
+// The tiles of one pair, in order.  dX: the cluster's tile (SPLIT, at most one
+// each) or pair, pair + pairs, ..  dW: likewise, but where the last round of dX
+// leaves pairs out, those first take `extra` tiles each, about as much work.
+struct GradIter {
+    int64_t n_x, n_w, pairs, pair, out0, extra, jx, jw;
+    __device__ GradIter(const GradArgs &p, int64_t cluster, int64_t part, int64_t clusters)
+        : n_x(p.tiles_x), n_w(2 * p.tiles_w), pairs(clusters * p.split), pair(cluster * p.split + part), jx(0), jw(0) {
+        if (p.split > 1) {
+            out0 = n_x * p.split;  // pairs of clusters without a tile of dX
+            jx = cluster < n_x ? cluster : n_x;
+        } else {
+            out0 = n_x % pairs == 0 ? pairs : n_x % pairs;
+            jx = pair;
+        }
+        const int64_t bx = 2 * ((p.R + 63) / 64) / p.split, bw = (p.T + 63) / 64;
+        extra = n_x == 0 ? 0 : bx / bw;
+        if (extra * (pairs - out0) > n_w) extra = 0;
+        split = p.split;
+    }
+    int split;
+    // false: no more.  is_x: a tile of dX; else src and the tile of dW
+    __device__ bool next(bool &is_x, int &src, int64_t &tile) {
+        src = 0;
+        if (jx < n_x) {
+            is_x = true;
+            tile = jx;
+            jx = split > 1 ? n_x : jx + pairs;
+            return true;
+        }
+        is_x = false;
+        const int64_t given = extra * (pairs - out0);  // handed out in advance
+        int64_t idx;
+        if (pair >= out0 && jw < extra)
+            idx = (pair - out0) * extra + jw;
+        else
+            idx = given + pair + (jw - (pair >= out0 ? extra : 0)) * pairs;
+        ++jw;
+        if (idx >= n_w) return false;
+        src = idx >= n_w / 2 ? 1 : 0;
+        tile = idx - src * (n_w / 2);
+        return true;
+    }
+};
+
+template <bool SPLIT>
 __global__ void __launch_bounds__(GradCfg::THREADS, 1)
     k_gemm_grad(const __grid_constant__ GradMaps tm, const __grid_constant__ GradArgs p) {
     using C = GradCfg;
@@ -141,15 +199,17 @@ __global__ void __launch_bounds__(GradCfg::THREADS, 1)
     uint8_t *epi_smem = smem + S * C::STAGE_BYTES;
     uint64_t *bars = reinterpret_cast<uint64_t *>(epi_smem + C::EPI_BYTES);
     uint64_t *full = bars, *empty = bars + S, *acc_full = bars + 2 * S, *acc_empty = acc_full + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_full + 4);
+    uint64_t *sum_ready = acc_full + 4, *sum_free = acc_full + 5;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_full + 6);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_ctarank();
-    const int64_t cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
-    const int64_t n_n = (p.N + 255) / 256, n_m = (p.M + 255) / 256;
-    const int64_t per = n_n * n_m;                                // tiles of one problem
-    const int64_t ntiles = KIND == GRAD_W ? 2 * per : per;
-    const int64_t nkb = KIND == GRAD_X ? 2 * p.nkb : p.nkb;
+    const uint32_t crank = cluster_ctarank(), rank = crank & 1u, leader = crank & ~1u;
+    const int split = SPLIT ? p.split : 1, part = SPLIT ? static_cast<int>(crank >> 1) : 0;
+    const int64_t cluster = blockIdx.x / (2 * split), nclusters = gridDim.x / (2 * split);
+    const int64_t n_n = (p.K + 255) / 256;                        // column tiles of every result
+    const int64_t m_x = (p.T + 255) / 256, m_w = (p.R + 255) / 256;
+    const int nkr = static_cast<int>((p.R + 63) / 64), nkt = static_cast<int>((p.T + 63) / 64);
+    const int x0 = static_cast<int>(2ll * nkr * part / split), x1 = static_cast<int>(2ll * nkr * (part + 1) / split);
     constexpr int64_t BAND = 16;  // row tiles per band of the tile order
 
     if (threadIdx.x == 0) {
@@ -161,10 +221,9 @@ __global__ void __launch_bounds__(GradCfg::THREADS, 1)
             mbar_init(&acc_full[b], 1);
             mbar_init(&acc_empty[b], 2 * C::EPI_WARPS);
         }
+        mbar_init(sum_ready, split * C::EPI_WARPS);
+        mbar_init(sum_free, split * C::EPI_WARPS);
         fence_barrier_init();
-        prefetch_tmap(&tm.a[0]);
-        prefetch_tmap(&tm.b[0]);
-        prefetch_tmap(&tm.c[0]);
     }
     if (warp == 1) {
         tmem_alloc_pair(tmem_slot, 512);
@@ -179,71 +238,94 @@ __global__ void __launch_bounds__(GradCfg::THREADS, 1)
 
     if (warp == 0) {
         // ---------------------------------------------------------- producer
-        if (lane == 0) {
-            int s = 0;
-            uint32_t ph = 0;
-            int64_t it = 0;
-            bool ok = true;
-            for (int64_t tile = cluster; tile < ntiles && ok; tile += nclusters) {
-                const int src = KIND == GRAD_W && tile >= per ? 1 : 0;
-                int64_t nt, mt;
-                tile_coords(tile - src * per, n_n, n_m, BAND, nt, mt);
-                const int32_t m0 = static_cast<int32_t>(mt * 256 + rank * 128);
-                const int32_t n0 = static_cast<int32_t>(nt * 256 + rank * 128);
-                for (int64_t v = 0; v < nkb; ++v) {
-                    if (it >= S && !mbar_wait(&empty[s], ph ^ 1u)) { ok = false; break; }
+        const bool lead = elect_one() != 0u;
+        const uint32_t st0 = smem_u32(smem), full0 = mapa_shared(full, leader);
+        int s = 0;
+        uint32_t ph = 0;
+        int64_t it = 0, tile;
+        bool ok = true, is_x, shared_sums = false;
+        int src;
+        GradIter tiles(p, cluster, part, nclusters);
+        while (ok && tiles.next(is_x, src, tile)) {
+            int64_t nt, mt;
+            tile_coords(tile, n_n, is_x ? m_x : m_w, BAND, nt, mt);
+            const int32_t m0 = static_cast<int32_t>(mt * 256 + rank * 128);
+            const int32_t n0 = static_cast<int32_t>(nt * 256 + rank * 128);
+            // SPLIT: the sums of the tile of dX lie over the stages until all have read them
+            if (SPLIT && shared_sums) {
+                if (!mbar_wait_cluster(sum_free, 0)) { ok = false; break; }
+                fence_proxy_async_smem();
+            }
+            shared_sums = SPLIT && is_x;
+            const int v1 = is_x ? x1 : nkt;
+            for (int v = is_x ? x0 : 0; v < v1; ++v, ++it) {
+                if (it >= S && !mbar_wait(&empty[s], ph ^ 1u)) { ok = false; break; }
+                if (lead) {
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * C::STAGE_BYTES);
-                    const uint32_t bar = mapa_shared(&full[s], 0);
-                    uint8_t *sa = smem + s * C::STAGE_BYTES, *sb = sa + C::A_BYTES;
-                    const int which = KIND == GRAD_W ? src : (v >= p.nkb ? 1 : 0);
-                    const int32_t k0 = static_cast<int32_t>((KIND == GRAD_X && which ? v - p.nkb : v) * 64);
-                    if (KIND == GRAD_X) {
-                        tma_load_2d_pair(sa, &tm.a[which], bar, k0, m0);
+                    const uint32_t bar = full0 + static_cast<uint32_t>(s) * 8u;
+                    const uint32_t sa = st0 + static_cast<uint32_t>(s) * C::STAGE_BYTES, sb = sa + C::A_BYTES;
+                    if (is_x) {
+                        const int which = v >= nkr ? 1 : 0;
+                        const int32_t k0 = (v - which * nkr) * 64;
+                        tma_load_2d_pair_at(sa, &tm.g[which], bar, k0, m0);
+                        tma_load_2d_pair_at(sb, &tm.w[which], bar, n0, k0);
+                        tma_load_2d_pair_at(sb + 8192, &tm.w[which], bar, n0 + 64, k0);
                     } else {
-                        tma_load_2d_pair(sa, &tm.a[which], bar, m0, k0);
-                        tma_load_2d_pair(sa + 8192, &tm.a[which], bar, m0 + 64, k0);
+                        tma_load_2d_pair_at(sa, &tm.gt[src], bar, m0, v * 64);
+                        tma_load_2d_pair_at(sa + 8192, &tm.gt[src], bar, m0 + 64, v * 64);
+                        tma_load_2d_pair_at(sb, &tm.x, bar, n0, v * 64);
+                        tma_load_2d_pair_at(sb + 8192, &tm.x, bar, n0 + 64, v * 64);
                     }
-                    const CUtensorMap *tb = &tm.b[KIND == GRAD_X ? which : 0];
-                    tma_load_2d_pair(sb, tb, bar, n0, k0);
-                    tma_load_2d_pair(sb + 8192, tb, bar, n0 + 64, k0);
-                    ++it;
-                    if (++s == S) { s = 0; ph ^= 1u; }
                 }
+                __syncwarp();
+                if (++s == S) { s = 0; ph ^= 1u; }
             }
-            if (!ok && rank == 0) {  // let copies already issued land before exiting
-                for (int64_t j = (it > S ? it - S : 0); j < it; ++j)
-                    mbar_wait(&full[j % S], static_cast<uint32_t>((j / S) & 1));
-            }
+        }
+        if (!ok && rank == 0) {  // let copies already issued land before exiting
+            for (int64_t j = (it > S ? it - S : 0); j < it; ++j)
+                mbar_wait(&full[j % S], static_cast<uint32_t>((j / S) & 1));
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA issuer
-        if (rank == 0 && lane == 0) {
+        if (rank == 0) {
+            const bool lead = elect_one() != 0u;
             // bits 15 and 16: A and B are MN-major
-            const uint32_t idesc = make_idesc_bf16(256, 256, false, 0) | (1u << 16) | (KIND == GRAD_W ? 1u << 15 : 0u);
+            const uint32_t idesc = make_idesc_bf16(256, 256, false, 0) | (1u << 16);
+            const uint16_t both = static_cast<uint16_t>(3u << leader);
+            const uint32_t st0 = smem_u32(smem);
+            const uint64_t ak = make_sdesc(st0, 16, 1024, 2), am = make_sdesc(st0, 8192, 1024, 2);
+            const uint64_t bm = make_sdesc(st0 + C::A_BYTES, 8192, 1024, 2);
             int s = 0;
             uint32_t ph = 0;
-            int64_t ti = 0;
-            bool ok = true;
-            for (int64_t tile = cluster; tile < ntiles && ok; tile += nclusters, ++ti) {
+            int64_t ti = 0, tile;
+            bool ok = true, is_x;
+            int src;
+            GradIter tiles(p, cluster, part, nclusters);
+            for (; ok && tiles.next(is_x, src, tile); ++ti) {
                 const int buf = static_cast<int>(ti & 1);
                 const uint32_t aph = static_cast<uint32_t>((ti >> 1) & 1);
                 if (ti >= 2 && !mbar_wait_cluster(&acc_empty[buf], aph ^ 1u)) break;
                 tc_fence_after();
                 const uint32_t dcol = tmem_base + static_cast<uint32_t>(buf * 256);
-                for (int64_t v = 0; v < nkb; ++v) {
+                const int n = is_x ? x1 - x0 : nkt;
+                const uint64_t ad = is_x ? ak : am, astep = is_x ? 32 >> 4 : 2048 >> 4;
+                const uint32_t id = idesc | (is_x ? 0u : 1u << 15);
+                for (int v = 0; v < n; ++v) {
                     if (!mbar_wait(&full[s], ph)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t a0 = smem_u32(smem + s * C::STAGE_BYTES), b0 = a0 + C::A_BYTES;
+                    const uint64_t so = static_cast<uint64_t>(static_cast<uint32_t>(s) * (C::STAGE_BYTES >> 4));
+                    if (lead) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        mma_bf16_pair(dcol,
-                                      KIND == GRAD_X ? make_sdesc(a0 + j * 32, 16, 1024, 2)
-                                                     : make_sdesc(a0 + j * 2048, 8192, 1024, 2),
-                                      make_sdesc(b0 + j * 2048, 8192, 1024, 2), idesc, (v > 0 || j > 0) ? 1u : 0u);
-                    mma_commit_pair(&empty[s]);
+                        for (int j = 0; j < 4; ++j)
+                            mma_bf16_pair(dcol, ad + so + j * astep, bm + so + j * (2048 >> 4), id,
+                                          (v > 0 || j > 0) ? 1u : 0u);
+                        mma_commit_pair_mask(&empty[s], both);
+                    }
+                    __syncwarp();
                     if (++s == S) { s = 0; ph ^= 1u; }
                 }
-                if (ok) mma_commit_pair(&acc_full[buf]);
+                if (ok && lead) mma_commit_pair_mask(&acc_full[buf], both);
+                __syncwarp();
             }
         }
     } else if (warp >= 4 && warp < 12) {
@@ -253,12 +335,14 @@ __global__ void __launch_bounds__(GradCfg::THREADS, 1)
         // the store's tensor map expects) and out by TMA
         const int q = warp & 3, h = (warp - 4) >> 2;
         uint8_t *out = epi_smem + (warp - 4) * 4096;
-        const uint32_t acc_empty_cl[2] = {mapa_shared(&acc_empty[0], 0), mapa_shared(&acc_empty[1], 0)};
-        int64_t ti = 0;
-        for (int64_t tile = cluster; tile < ntiles; tile += nclusters, ++ti) {
-            const int src = KIND == GRAD_W && tile >= per ? 1 : 0;
+        const uint32_t acc_empty0 = mapa_shared(&acc_empty[0], leader), acc_empty1 = mapa_shared(&acc_empty[1], leader);
+        int64_t ti = 0, tile;
+        bool is_x;
+        int src;
+        GradIter tiles(p, cluster, part, nclusters);
+        for (; tiles.next(is_x, src, tile); ++ti) {
             int64_t nt, mt;
-            tile_coords(tile - src * per, n_n, n_m, BAND, nt, mt);
+            tile_coords(tile, n_n, is_x ? m_x : m_w, BAND, nt, mt);
             const int buf = static_cast<int>(ti & 1);
             if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], static_cast<uint32_t>((ti >> 1) & 1)))) break;
             tc_fence_after();
@@ -266,8 +350,71 @@ __global__ void __launch_bounds__(GradCfg::THREADS, 1)
                                 static_cast<uint32_t>(buf * 256 + h * 128);
             const int64_t row = mt * 256 + rank * 128 + q * 32 + lane;
             const int64_t col0 = nt * 256 + h * 128;
-            const uint32_t *mrow = KIND == GRAD_W && p.mask[src] != nullptr && row < p.M
-                                       ? p.mask[src] + row * p.mask_words : nullptr;
+            if constexpr (SPLIT) {
+                if (is_x) {
+                    // [4 columns][row][column] fp32 over the stages, which are idle: every
+                    // load of the tile has been used
+                    float4 *mine = reinterpret_cast<float4 *>(smem) + (h * 32) * 128 + q * 32 + lane;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(tb + c * 32, v);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            mine[(c * 8 + i) * 128] = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                                                  __uint_as_float(v[4 * i + 2]),
+                                                                  __uint_as_float(v[4 * i + 3]));
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(buf ? acc_empty1 : acc_empty0);
+                    if (lane < split) mbar_arrive_cluster(mapa_shared(sum_ready, 2 * lane + rank));
+                    if (!__all_sync(0xffffffffu, mbar_wait_cluster(sum_ready, 0))) break;
+                    const uint32_t off = smem_u32(mine);
+                    uint32_t from[C::MAX_SPLIT];
+#pragma unroll
+                    for (int i = 0; i < C::MAX_SPLIT; ++i)
+                        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                                     : "=r"(from[i]) : "r"(off), "r"(2 * (i < split ? i : part) + rank));
+#pragma unroll 1
+                    for (int g = 32 * part / split; g < 32 * (part + 1) / split; ++g) {  // this pair's columns
+                        float4 pv[C::MAX_SPLIT];
+#pragma unroll
+                        for (int i = 0; i < C::MAX_SPLIT; ++i)
+                            if (i < split) pv[i] = ld_dsmem_f32x4(from[i] + static_cast<uint32_t>(g * 2048));
+                        float4 f = pv[0];
+#pragma unroll
+                        for (int i = 1; i < C::MAX_SPLIT; ++i)
+                            if (i < split) {
+                                f.x += pv[i].x;
+                                f.y += pv[i].y;
+                                f.z += pv[i].z;
+                                f.w += pv[i].w;
+                            }
+                        const int64_t col = col0 + g * 4;
+                        if (row < p.T && col < p.K) {
+                            const uint32_t lo = pack_bf16x2(f.x, f.y), hi = pack_bf16x2(f.z, f.w);
+                            uint16_t *dst = p.dX + row * p.lddx + col;
+                            if (col + 4 <= p.K) {
+                                *reinterpret_cast<uint2 *>(dst) = make_uint2(lo, hi);
+                            } else {
+                                dst[0] = static_cast<uint16_t>(lo & 0xFFFFu);
+                                if (col + 1 < p.K) dst[1] = static_cast<uint16_t>(lo >> 16);
+                                if (col + 2 < p.K) dst[2] = static_cast<uint16_t>(hi & 0xFFFFu);
+                            }
+                        }
+                    }
+                    __syncwarp();
+                    fence_proxy_async_smem();  // the stages go back to TMA
+                    if (lane < split) mbar_arrive_cluster(mapa_shared(sum_free, 2 * lane + rank));
+                    continue;
+                }
+            }
+            const uint32_t *mrow = !is_x && p.mask[src] != nullptr && row < p.R ? p.mask[src] + row * p.mask_words
+                                                                                 : nullptr;
+            const int64_t rows = is_x ? p.T : p.R;
+            const CUtensorMap *tc = is_x ? &tm.dx : (src ? &tm.dw[1] : &tm.dw[0]);
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 uint32_t v[64], w[32];
@@ -284,15 +431,13 @@ __global__ void __launch_bounds__(GradCfg::THREADS, 1)
                 if (c == 1) {
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive_cluster(acc_empty_cl[buf]);
+                    if (lane == 0) mbar_arrive_cluster(buf ? acc_empty1 : acc_empty0);
                 }
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     uint32_t x = pack_bf16x2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                    if (KIND == GRAD_W) {
-                        const uint32_t kb = keep[i >> 4] >> (2 * (i & 15));
-                        x &= ((kb & 1u) ? 0xFFFFu : 0u) | ((kb & 2u) ? 0xFFFF0000u : 0u);
-                    }
+                    const uint32_t kb = keep[i >> 4] >> (2 * (i & 15));
+                    x &= ((kb & 1u) ? 0xFFFFu : 0u) | ((kb & 2u) ? 0xFFFF0000u : 0u);
                     w[i] = x;
                 }
                 if (lane == 0) bulk_wait_group_read0();
@@ -303,8 +448,8 @@ __global__ void __launch_bounds__(GradCfg::THREADS, 1)
                         make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0 && mt * 256 + rank * 128 + q * 32 < p.M && col0 + c * 64 < p.N) {
-                    tma_store_2d(&tm.c[src], out, static_cast<int32_t>(col0 + c * 64),
+                if (lane == 0 && mt * 256 + rank * 128 + q * 32 < rows && col0 + c * 64 < p.K) {
+                    tma_store_2d(tc, out, static_cast<int32_t>(col0 + c * 64),
                                  static_cast<int32_t>(mt * 256 + rank * 128 + q * 32));
                     bulk_commit_group();
                 }
@@ -315,7 +460,7 @@ __global__ void __launch_bounds__(GradCfg::THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();
+    cluster_sync_all();  // also: no CTA leaves while another reads its sums
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, 512);
@@ -389,26 +534,80 @@ size_t grad_bytes(int64_t T, int64_t R) {  // one of dG, dU
     return (static_cast<size_t>(T) * static_cast<size_t>(padded8(R)) * 2 + 255) / 256 * 256;
 }
 
-template <int KIND>
-nm_status launch_grad(const GradMaps &maps, const GradArgs &p, int64_t ntiles, cudaStream_t s) {
+// clusters of 2 * split blocks that can be resident at once on the current
+// device (0: none, or a CUDA error), cached per device
+template <auto kernel>
+int64_t grad_clusters(int split) {
     using Cfg = GradCfg;
-    if (!set_smem_attr<k_gemm_grad<KIND>>(Cfg::SMEM_BYTES)) return NM_ERR_CUDA;
-    const int64_t pairs = sm_count() / 2;
+    static int cache[64][Cfg::MAX_SPLIT + 1] = {};  // count + 1
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (cache[dev][split] == 0) {
+        if (!set_smem_attr<kernel>(Cfg::SMEM_BYTES)) return 0;
+        if (split > 4 &&
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+            cudaGetLastError();
+            return 0;
+        }
+        cudaLaunchConfig_t q = {};
+        q.gridDim = dim3(static_cast<unsigned>(2 * split * (sm_count() / (2 * split))), 1, 1);
+        q.blockDim = dim3(Cfg::THREADS, 1, 1);
+        q.dynamicSmemBytes = Cfg::SMEM_BYTES;
+        cudaLaunchAttribute qa[1];
+        qa[0].id = cudaLaunchAttributeClusterDimension;
+        qa[0].val.clusterDim.x = static_cast<unsigned>(2 * split);
+        qa[0].val.clusterDim.y = 1;
+        qa[0].val.clusterDim.z = 1;
+        q.attrs = qa;
+        q.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &q) != cudaSuccess) {
+            cudaGetLastError();
+            n = 0;
+        }
+        cache[dev][split] = n + 1;
+    }
+    return cache[dev][split] - 1;
+}
+
+nm_status launch_grad(const GradMaps &maps, GradArgs p, cudaStream_t s) {
+    using Cfg = GradCfg;
+    // pairs per tile of dX: the least of (contraction blocks of a pair) x ~600
+    // clocks + the exchange of 128 KB of sums at some 18 bytes a clock
+    int split = 1;
+    int64_t clusters = grad_clusters<k_gemm_grad<false>>(1);
+    const int64_t blocks = 2 * ((p.R + 63) / 64);
+    int64_t best = blocks * 600;
+    for (int i = 2; i <= Cfg::MAX_SPLIT && p.tiles_x > 0 && i <= blocks; ++i) {
+        const int64_t cost = (blocks + i - 1) / i * 600 + 10000;
+        if (cost >= best) continue;
+        const int64_t n = grad_clusters<k_gemm_grad<true>>(i);
+        if (n < p.tiles_x) continue;
+        best = cost;
+        split = i;
+        clusters = n;
+    }
+    if (clusters < 1) return NM_ERR_CUDA;
+    const int64_t want = split > 1 ? p.tiles_x + (2 * p.tiles_w + split - 1) / split : p.tiles_x + 2 * p.tiles_w;
+    if (clusters > want) clusters = want;
+    p.split = split;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * (ntiles < pairs ? ntiles : pairs)), 1, 1);
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * split * clusters), 1, 1);
     cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
     cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(2 * split);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, k_gemm_grad<KIND>, maps, p) != cudaSuccess) return NM_ERR_CUDA;
+    const cudaError_t e = split > 1 ? cudaLaunchKernelEx(&cfg, k_gemm_grad<true>, maps, p)
+                                    : cudaLaunchKernelEx(&cfg, k_gemm_grad<false>, maps, p);
+    if (e != cudaSuccess) return NM_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
 }
 
@@ -444,45 +643,40 @@ extern "C" nm_status nm_sparse_glu_backward(const uint16_t *dH, int64_t lddh, co
     uint16_t *dU = reinterpret_cast<uint16_t *>(static_cast<uint8_t *>(ws) + grad_bytes(T, R));
     const int64_t ldd = padded8(R);
 
-    GradMaps mx{}, mw{};
-    if (dX && (!make_tmap_bf16(&mx.a[0], dG, T, R, ldd, 64, 128, true) ||
-               !make_tmap_bf16(&mx.a[1], dU, T, R, ldd, 64, 128, true) ||
-               !make_tmap_bf16(&mx.b[0], Wg, R, K, ldw, 64, 64, true) ||
-               !make_tmap_bf16(&mx.b[1], Wu, R, K, ldw, 64, 64, true) ||
-               !make_tmap_bf16(&mx.c[0], dX, T, K, lddx, 64, 32, true)))
-        return NM_ERR_CUDA;
-    if (need_w && (!make_tmap_bf16(&mw.a[0], dG, T, R, ldd, 64, 64, true) ||
-                   !make_tmap_bf16(&mw.a[1], dU, T, R, ldd, 64, 64, true) ||
-                   !make_tmap_bf16(&mw.b[0], X, T, K, ldx, 64, 64, true) ||
-                   !make_tmap_bf16(&mw.c[0], dWg, R, K, lddw, 64, 32, true) ||
-                   !make_tmap_bf16(&mw.c[1], dWu, R, K, lddw, 64, 32, true)))
-        return NM_ERR_CUDA;
+    GradMaps maps{};
+    GradArgs p{};
+    p.T = T;
+    p.R = R;
+    p.K = K;
+    if (dX) {
+        if (!make_tmap_bf16(&maps.g[0], dG, T, R, ldd, 64, 128, true) ||
+            !make_tmap_bf16(&maps.g[1], dU, T, R, ldd, 64, 128, true) ||
+            !make_tmap_bf16(&maps.w[0], Wg, R, K, ldw, 64, 64, true) ||
+            !make_tmap_bf16(&maps.w[1], Wu, R, K, ldw, 64, 64, true) ||
+            !make_tmap_bf16(&maps.dx, dX, T, K, lddx, 64, 32, true))
+            return NM_ERR_CUDA;
+        p.tiles_x = ((T + 255) / 256) * ((K + 255) / 256);
+        p.dX = dX;
+        p.lddx = lddx;
+    }
+    if (need_w) {
+        if (!make_tmap_bf16(&maps.gt[0], dG, T, R, ldd, 64, 64, true) ||
+            !make_tmap_bf16(&maps.gt[1], dU, T, R, ldd, 64, 64, true) ||
+            !make_tmap_bf16(&maps.x, X, T, K, ldx, 64, 64, true) ||
+            !make_tmap_bf16(&maps.dw[0], dWg, R, K, lddw, 64, 32, true) ||
+            !make_tmap_bf16(&maps.dw[1], dWu, R, K, lddw, 64, 32, true))
+            return NM_ERR_CUDA;
+        p.tiles_w = ((R + 255) / 256) * ((K + 255) / 256);
+        p.mask[0] = mask_gate;
+        p.mask[1] = mask_up;
+        p.mask_words = mask_gate ? ((K + m - 1) / m * m + 31) / 32 : 0;
+    }
     const int64_t chunks = (R + 7) / 8;
     dim3 grid(static_cast<unsigned>((chunks + 255) / 256), static_cast<unsigned>(T < 65535 ? T : 65535),
               static_cast<unsigned>((T + 65534) / 65535));
     k_glu_grad<<<grid, 256, 0, s>>>(dH, lddh, G, U, ldgu, T, R, act, dG, dU, ldd);
     if (cudaGetLastError() != cudaSuccess) return NM_ERR_CUDA;
-    if (dX) {
-        GradArgs p{};
-        p.M = T;
-        p.N = K;
-        p.nkb = (R + 63) / 64;
-        mx.c[1] = mx.c[0];
-        const nm_status st = launch_grad<GRAD_X>(mx, p, ((T + 255) / 256) * ((K + 255) / 256), s);
-        if (st != NM_OK) return st;
-    }
-    if (need_w) {
-        GradArgs p{};
-        p.M = R;
-        p.N = K;
-        p.nkb = (T + 63) / 64;
-        p.mask[0] = mask_gate;
-        p.mask[1] = mask_up;
-        p.mask_words = mask_gate ? ((K + m - 1) / m * m + 31) / 32 : 0;
-        mw.b[1] = mw.b[0];
-        return launch_grad<GRAD_W>(mw, p, 2 * ((R + 255) / 256) * ((K + 255) / 256), s);
-    }
-    return NM_OK;
+    return launch_grad(maps, p, s);
 }
 
 extern "C" nm_status nm_sparse_densify(const uint16_t *vals, const uint32_t *mask, int64_t R, int64_t K, int n, int m,
