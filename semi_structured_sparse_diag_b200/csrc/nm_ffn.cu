@@ -43,6 +43,8 @@ struct FfnCfg {
     static constexpr int BAR_BYTES = 256;
     static constexpr int SMEM_BYTES = 232448;
     static constexpr int SMEM_DATA = (SMEM_BYTES - BAR_BYTES - 1024) / 1024 * 1024;
+    // without a split: the epilogue's output staging, two buffers of 1 KB a warp
+    static constexpr int OUT_BYTES = EPI_WARPS * 2048, OFF_OUT = SMEM_DATA - OUT_BYTES;
     static constexpr int TMEM_COLS = 512;
     static constexpr int TMEM_D0 = 0, TMEM_E0 = 240, TMEM_E1 = 248, TMEM_D1 = 256;
     static_assert(OFF_B % 1024 == 0, "operand alignment");
@@ -74,12 +76,28 @@ struct FfnArgs {
     int rb, width;
 };
 
-__device__ __forceinline__ float act_of(float g, int act) {
-    // silu g / (1 + e^-g); gelu (tanh form) g / (1 + e^-2z), since
-    // (1 + tanh z) / 2 = 1 / (1 + e^-2z); e^x overflowing to inf gives 0
-    if (act == ACT_RELU2) return g < 0.0f ? 0.0f : g * g;
-    const float z = act == ACT_SILU ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g);
+// silu g / (1 + e^-g); gelu (tanh form) g / (1 + e^-2z), since (1 + tanh z) / 2 =
+// 1 / (1 + e^-2z); e^x overflowing to inf gives 0; max(g, 0)^2 keeps a NaN
+template <int ACT>
+__device__ __forceinline__ float act_fn(float g) {
+    if (ACT == ACT_RELU2) return g < 0.0f ? 0.0f : g * g;
+    const float z = ACT == ACT_SILU ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g);
     return __fdividef(g, 1.0f + __expf(-z));
+}
+
+// g[i] = act(g[i]) u[i]
+template <int N>
+__device__ __forceinline__ void gate(float (&g)[N], const float (&u)[N], int act) {
+    if (act == ACT_SILU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) g[i] = act_fn<ACT_SILU>(g[i]) * u[i];
+    } else if (act == ACT_GELU) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) g[i] = act_fn<ACT_GELU>(g[i]) * u[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) g[i] = act_fn<ACT_RELU2>(g[i]) * u[i];
+    }
 }
 
 // A cluster of `split` pairs computes a tile: pair j takes the j-th part of its
@@ -441,81 +459,106 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
                                 }
                         }
                         const int t = (g + u * gstep) * 4;
+                        if (OP == OP_GLU && p.G != nullptr && rok) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                if (t + j < nv) {
+                                    const int64_t at = (tok0 + t + j) * p.ldgu + row;
+                                    p.G[at] = static_cast<uint16_t>(pack_bf16x2(f[0][j], 0.0f));
+                                    p.U[at] = static_cast<uint16_t>(pack_bf16x2(f[NACC - 1][j], 0.0f));
+                                }
+                        }
+                        if (OP == OP_GLU) gate(f[0], f[NACC - 1], p.act);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
-                            if (t + j < nv && rok) {
-                                const int64_t tk = tok0 + t + j;
-                                if (OP == OP_GLU) {
-                                    if (p.G != nullptr) {
-                                        p.G[tk * p.ldgu + row] = static_cast<uint16_t>(pack_bf16x2(f[0][j], 0.0f));
-                                        p.U[tk * p.ldgu + row] = static_cast<uint16_t>(pack_bf16x2(f[NACC - 1][j], 0.0f));
-                                    }
-                                    f[0][j] = act_of(f[0][j], p.act) * f[NACC - 1][j];
-                                }
-                                p.Y[tk * p.ldy + row] = static_cast<uint16_t>(pack_bf16x2(f[0][j], 0.0f));
-                            }
+                            if (t + j < nv && rok)
+                                p.Y[(tok0 + t + j) * p.ldy + row] = static_cast<uint16_t>(pack_bf16x2(f[0][j], 0.0f));
                     }
                 }
                 __syncwarp();
                 if (lane < split) mbar_arrive_cluster(mapa_shared(sum_free, 2 * lane + rank));
             }
             if constexpr (!SPLIT) {
-                uint32_t pk[8][8];
-                // two passes of eight chunks (OP_GLU: one); the accumulator is released
-                // once the last chunk is in registers, before its stores
-#pragma unroll 1
-                for (int c8 = c_lo; c8 < c_hi || c8 == c_lo; c8 += 8) {
+                // 32 rows x 16 tokens at a time, as 8 x 8 blocks: out of tensor memory in
+                // the layout of a matrix fragment, transposed by stmatrix on the way to
+                // the warp's 1 KB of shared memory ([token][32 rows], 16-byte pieces
+                // swizzled against bank conflicts), and out as 64 bytes a token.  (Two-byte
+                // stores straight from registers, a row to each lane, took as long as the
+                // tile's products: 820 us for 8192 tokens against TODO.)  The accumulators
+                // are released once the last chunk is in registers.
+                const int64_t row0 = mt * tile_rows + acc0 * 256 + rank * 128 + q * 32;
+                const uint32_t stage_out = smem_u32(smem) + C::OFF_OUT + static_cast<uint32_t>(warp - 4) * 2048u;
+                const int bi = lane >> 3, st_tok = (lane & 7) + 8 * (bi >> 1);
+                uint32_t st_at[2];  // where this lane's row of the blocks of lanes 0..15, 16..31 goes
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int c = c8 + k;
-                        if (c < c_hi) {
-                            float f[NACC][16];
-                            load_chunk(c, f);
-                            if (OP == OP_GLU) {
-                                const int64_t t = tok0 + c * 16;
-                                if (p.G != nullptr && rok) {
-                                    uint16_t *gp = p.G + t * p.ldgu + row, *up = p.U + t * p.ldgu + row;
+                for (int u = 0; u < 2; ++u)
+                    st_at[u] = static_cast<uint32_t>(st_tok * 64 + ((((bi & 1) + 2 * u) ^ ((st_tok >> 1) & 3)) << 4));
+                uint32_t flip = 0;  // two buffers in turn: one sync orders writes after the reads before the last
+                auto emit = [&](uint16_t *dst, int64_t ld, int c, const float (&f)[16]) {
+                    const uint32_t buf = stage_out + flip;
+                    flip ^= 1024u;
 #pragma unroll
-                                    for (int j = 0; j < 16; j += 2) {
-                                        const uint32_t g2 = pack_bf16x2(f[0][j], f[0][j + 1]);
-                                        const uint32_t u2 = pack_bf16x2(f[NACC - 1][j], f[NACC - 1][j + 1]);
-                                        if (c * 16 + j < nv) {
-                                            gp[j * p.ldgu] = static_cast<uint16_t>(g2 & 0xFFFFu);
-                                            up[j * p.ldgu] = static_cast<uint16_t>(u2 & 0xFFFFu);
-                                        }
-                                        if (c * 16 + j + 1 < nv) {
-                                            gp[(j + 1) * p.ldgu] = static_cast<uint16_t>(g2 >> 16);
-                                            up[(j + 1) * p.ldgu] = static_cast<uint16_t>(u2 >> 16);
-                                        }
-                                    }
-                                }
+                    for (int u = 0; u < 2; ++u)
+                        stmatrix_x4_trans(buf + st_at[u], pack_bf16x2(f[8 * u], f[8 * u + 1]),
+                                          pack_bf16x2(f[8 * u + 2], f[8 * u + 3]), pack_bf16x2(f[8 * u + 4], f[8 * u + 5]),
+                                          pack_bf16x2(f[8 * u + 6], f[8 * u + 7]));
+                    __syncwarp();
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) f[0][j] = act_of(f[0][j], p.act) * f[NACC - 1][j];
+                    for (int u = 0; u < 2; ++u) {
+                        const int tok = (lane >> 2) + 8 * u, piece = lane & 3;
+                        uint4 v;
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                     : "r"(buf + static_cast<uint32_t>(tok * 64 + ((piece ^ ((tok >> 1) & 3)) << 4))));
+                        const int64_t r = row0 + piece * 8;
+                        if (c * 16 + tok < nv && r < p.R) {
+                            uint16_t *o = dst + (tok0 + c * 16 + tok) * ld + r;
+                            if (r + 8 <= p.R) {
+                                *reinterpret_cast<uint4 *>(o) = v;
+                            } else {
+                                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                                for (int e = 0; e < 8; ++e)
+                                    if (r + e < p.R) o[e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
                             }
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) pk[k][i] = pack_bf16x2(f[0][2 * i], f[0][2 * i + 1]);
                         }
                     }
-                    if (c8 + 8 >= c_hi) {
+                };
+                auto fetch = [&](int c, uint32_t (&v)[NACC][2][8]) {
+#pragma unroll
+                    for (int a = 0; a < NACC; ++a)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+                            tmem_ld_16x256b_x2(tacc[a] + (static_cast<uint32_t>(u * 16) << 16) + c * 16, v[a][u]);
+                };
+                uint32_t v[NACC][2][8];
+                if (c_lo < c_hi) fetch(c_lo, v);
+#pragma unroll 1
+                for (int c = c_lo; c < c_hi; ++c) {
+                    tmem_ld_wait();
+                    float f[NACC][16];
+#pragma unroll
+                    for (int a = 0; a < NACC; ++a)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) f[a][j] = __uint_as_float(v[a][j >> 3][j & 7]);
+                    if (c + 1 < c_hi) fetch(c + 1, v);
+                    if (c + 1 == c_hi) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(acc_empty_cl);
                     }
-                    if (rok) {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int c = c8 + k;
-                            if (c < c_hi) {
-                                uint16_t *yp = p.Y + (tok0 + c * 16) * p.ldy + row;
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) {
-                                    if (c * 16 + 2 * i < nv) yp[0] = static_cast<uint16_t>(pk[k][i] & 0xFFFFu);
-                                    if (c * 16 + 2 * i + 1 < nv) yp[p.ldy] = static_cast<uint16_t>(pk[k][i] >> 16);
-                                    yp += 2 * p.ldy;
-                                }
-                            }
+                    if (OP == OP_GLU) {
+                        if (p.G != nullptr) {
+                            emit(p.G, p.ldgu, c, f[0]);
+                            emit(p.U, p.ldgu, c, f[NACC - 1]);
                         }
+                        gate(f[0], f[NACC - 1], p.act);
                     }
+                    emit(p.Y, p.ldy, c, f[0]);
+                }
+                if (c_lo >= c_hi) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_cluster(acc_empty_cl);
                 }
             }
         }
@@ -943,7 +986,7 @@ bool ffn_search(int64_t T, int64_t Rpad, int64_t nkb, FfnPlan *best) {
             const int rows = OP == OP_GLU || accs == 1 ? 256 : 512;
             const int64_t tiles = (T + bn - 1) / bn * ((Rpad + rows - 1) / rows), rounds = (tiles + clusters - 1) / clusters;
             const int sb = Cfg::stage_bytes(bn);
-            int room = Cfg::SMEM_DATA, off = 0;
+            int room = split > 1 ? Cfg::SMEM_DATA : Cfg::OFF_OUT, off = 0;
             if (split > 1) {  // one round: the sums lie over the idle stages
                 if (Cfg::sum_bytes(bn) > Cfg::SMEM_DATA) continue;
                 if (rounds > 1) room -= Cfg::sum_bytes(bn);
