@@ -31,6 +31,11 @@ namespace nm {
 enum { OP_GLU = 0, OP_LORA = 1 };
 enum { ACT_SILU = 0, ACT_GELU = 1, ACT_RELU2 = 2 };
 
+// epilogue warps: what a tile waits for is their latency, so the plain kernel has
+// sixteen; the exchange of a split needs more registers than that leaves
+constexpr int ffn_epi_warps(bool split) { return split ? 8 : 16; }
+constexpr int ffn_threads(bool split) { return 128 + 32 * ffn_epi_warps(split); }
+
 struct FfnCfg {
     static constexpr int BN_MAX = 240;          // tokens per tile (both CTAs)
     static constexpr int A_BYTES = BM * 128;    // 128 rows x 64 values
@@ -38,13 +43,11 @@ struct FfnCfg {
     static constexpr int OFF_B = OFF_E1 + EBLK_BYTES;  // two atoms of bn/2 tokens x 64 columns
     static constexpr int MAX_STAGES = 6;
     static constexpr int MAX_SPLIT = 8;         // CTA pairs that share a tile's K' blocks
-    static constexpr int EPI_WARPS = 8;
-    static constexpr int THREADS = 384;
     static constexpr int BAR_BYTES = 256;
     static constexpr int SMEM_BYTES = 232448;
     static constexpr int SMEM_DATA = (SMEM_BYTES - BAR_BYTES - 1024) / 1024 * 1024;
-    // without a split: the epilogue's output staging, two buffers of 1 KB a warp
-    static constexpr int OUT_BYTES = EPI_WARPS * 2048, OFF_OUT = SMEM_DATA - OUT_BYTES;
+    // without a split: the epilogue's output staging, 1 KB a warp
+    static constexpr int OUT_BYTES = ffn_epi_warps(false) * 1024, OFF_OUT = SMEM_DATA - OUT_BYTES;
     static constexpr int TMEM_COLS = 512;
     static constexpr int TMEM_D0 = 0, TMEM_E0 = 240, TMEM_E1 = 248, TMEM_D1 = 256;
     static_assert(OFF_B % 1024 == 0, "operand alignment");
@@ -111,9 +114,10 @@ __device__ __forceinline__ void gate(float (&g)[N], const float (&u)[N], int act
 // in the plain epilogue, which held up the next tile: 850 -> 1390 us for the
 // gate and up projections of 8192 tokens.)
 template <int MODE, int OP, bool SPLIT>
-__global__ void __launch_bounds__(FfnCfg::THREADS, 1)
+__global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
     k_ffn(const __grid_constant__ FfnMaps tm, const __grid_constant__ FfnArgs p) {
     using C = FfnCfg;
+    constexpr int EPI_WARPS = ffn_epi_warps(SPLIT);
     const int S = p.stages;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -154,9 +158,9 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
             mbar_init(&empty[s], 1);
         }
         mbar_init(acc_full, 1);
-        mbar_init(acc_empty, 2 * C::EPI_WARPS);
-        mbar_init(sum_ready, split * C::EPI_WARPS);
-        mbar_init(sum_free, split * C::EPI_WARPS);
+        mbar_init(acc_empty, 2 * EPI_WARPS);
+        mbar_init(sum_ready, split * EPI_WARPS);
+        mbar_init(sum_free, split * EPI_WARPS);
         fence_barrier_init();
         prefetch_tmap(&tm.a0);
         prefetch_tmap(&tm.e0);
@@ -350,13 +354,13 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
                 __syncwarp();
             }
         }
-    } else if (warp >= 4 && warp < 12) {
+    } else if (warp >= 4) {
         // ---------------------------------------------------------- epilogue
-        // a warp = lane quarter q x half h: of the tokens where one warp needs both
-        // accumulators (OP_GLU) or there is but one (256 rows a tile), else h is
-        // the accumulator
-        const int q = warp & 3, h = (warp - 4) >> 2;
-        constexpr int NACC = OP == OP_GLU ? 2 : 1;
+        // a warp = lane quarter q x a part of the tokens, and of both accumulators
+        // where one warp needs both (OP_GLU), or of one of them: then half of the
+        // parts are of each accumulator, if there are two
+        const int q = warp & 3, grp = (warp - 4) >> 2;
+        constexpr int NACC = OP == OP_GLU ? 2 : 1, GRPS = EPI_WARPS / 4;
         const bool by_tokens = OP == OP_GLU || tile_rows == 256;
         const uint32_t acc_empty_cl = mapa_shared(acc_empty, leader);
         int64_t ti = 0;
@@ -366,20 +370,15 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
             if (!__all_sync(0xffffffffu, mbar_wait(acc_full, static_cast<uint32_t>(ti & 1)))) break;
             tc_fence_after();
             const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
-            const int acc0 = by_tokens ? 0 : h;  // the (first) accumulator of this warp
+            const int acc0 = by_tokens ? 0 : grp & 1;  // the (first) accumulator of this warp
+            const int tp = by_tokens ? grp : grp >> 1, ntp = by_tokens ? GRPS : GRPS / 2;  // its part of the tokens
             const uint32_t tacc[2] = {tq + (acc0 ? C::TMEM_D1 : C::TMEM_D0), tq + C::TMEM_D1};
             const int64_t tok0 = nt * bn;
             const int nv = static_cast<int>(T - tok0 < bn ? T - tok0 : bn);  // real tokens of the tile
             const int nch = (nv + 15) / 16;                                  // their chunks of 16
-            int c_lo = 0, c_hi = nch;
             const bool active = acc0 == 0 || second(mt);
-            if (by_tokens) {
-                const int half = (bn / 16 + 1) / 2;
-                c_lo = h ? half : 0;
-                c_hi = h ? nch : (nch < half ? nch : half);
-            } else if (!active) {
-                c_hi = 0;
-            }
+            const int per = (bn / 16 + ntp - 1) / ntp, c_lo = tp * per;
+            const int c_hi = !active ? c_lo : (c_lo + per < nch ? c_lo + per : nch);
             // 16 tokens of the accumulators
             auto load_chunk = [&](int c, float (&f)[NACC][16]) {
                 uint32_t v[NACC][16];
@@ -418,7 +417,7 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
                 // GROUPS x 4 tokens are in flight before the first is used
                 constexpr int GROUPS = OP == OP_GLU ? 1 : 2;
                 const int ng = (nv + 3) / 4, g1 = active ? ng * (part + 1) / split : 0;
-                const int gstep = by_tokens ? 2 : 1;
+                const int gstep = ntp;
                 const uint32_t off = smem_u32(mine);
                 uint32_t from[C::MAX_SPLIT];
 #pragma unroll
@@ -426,7 +425,7 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
                     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
                                  : "=r"(from[i]) : "r"(off), "r"(2 * (i < split ? i : part) + rank));
 #pragma unroll 1
-                for (int g = ng * part / split + (by_tokens ? h : 0); g < g1; g += gstep * GROUPS) {
+                for (int g = ng * part / split + tp; g < g1; g += gstep * GROUPS) {
                     float4 pv[C::MAX_SPLIT][GROUPS][NACC];
 #pragma unroll
                     for (int i = 0; i < C::MAX_SPLIT; ++i)
@@ -487,16 +486,14 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
                 // tile's products: 820 us for 8192 tokens against TODO.)  The accumulators
                 // are released once the last chunk is in registers.
                 const int64_t row0 = mt * tile_rows + acc0 * 256 + rank * 128 + q * 32;
-                const uint32_t stage_out = smem_u32(smem) + C::OFF_OUT + static_cast<uint32_t>(warp - 4) * 2048u;
+                const uint32_t buf = smem_u32(smem) + C::OFF_OUT + static_cast<uint32_t>(warp - 4) * 1024u;
                 const int bi = lane >> 3, st_tok = (lane & 7) + 8 * (bi >> 1);
                 uint32_t st_at[2];  // where this lane's row of the blocks of lanes 0..15, 16..31 goes
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
                     st_at[u] = static_cast<uint32_t>(st_tok * 64 + ((((bi & 1) + 2 * u) ^ ((st_tok >> 1) & 3)) << 4));
-                uint32_t flip = 0;  // two buffers in turn: one sync orders writes after the reads before the last
                 auto emit = [&](uint16_t *dst, int64_t ld, int c, const float (&f)[16]) {
-                    const uint32_t buf = stage_out + flip;
-                    flip ^= 1024u;
+                    __syncwarp();  // the piece before has been read
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
                         stmatrix_x4_trans(buf + st_at[u], pack_bf16x2(f[8 * u], f[8 * u + 1]),
@@ -524,29 +521,25 @@ __global__ void __launch_bounds__(FfnCfg::THREADS, 1)
                         }
                     }
                 };
-                auto fetch = [&](int c, uint32_t (&v)[NACC][2][8]) {
+#pragma unroll 1
+                for (int c = c_lo; c < c_hi; ++c) {
+                    uint32_t v[NACC][2][8];
 #pragma unroll
                     for (int a = 0; a < NACC; ++a)
 #pragma unroll
                         for (int u = 0; u < 2; ++u)
                             tmem_ld_16x256b_x2(tacc[a] + (static_cast<uint32_t>(u * 16) << 16) + c * 16, v[a][u]);
-                };
-                uint32_t v[NACC][2][8];
-                if (c_lo < c_hi) fetch(c_lo, v);
-#pragma unroll 1
-                for (int c = c_lo; c < c_hi; ++c) {
                     tmem_ld_wait();
-                    float f[NACC][16];
-#pragma unroll
-                    for (int a = 0; a < NACC; ++a)
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) f[a][j] = __uint_as_float(v[a][j >> 3][j & 7]);
-                    if (c + 1 < c_hi) fetch(c + 1, v);
                     if (c + 1 == c_hi) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(acc_empty_cl);
                     }
+                    float f[NACC][16];
+#pragma unroll
+                    for (int a = 0; a < NACC; ++a)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) f[a][j] = __uint_as_float(v[a][j >> 3][j & 7]);
                     if (OP == OP_GLU) {
                         if (p.G != nullptr) {
                             emit(p.G, p.ldgu, c, f[0]);
@@ -931,7 +924,7 @@ int64_t ffn_clusters_of(int split) {
         }
         cudaLaunchConfig_t q = {};
         q.gridDim = dim3(static_cast<unsigned>(2 * split * (sm_count() / (2 * split))), 1, 1);
-        q.blockDim = dim3(Cfg::THREADS, 1, 1);
+        q.blockDim = dim3(ffn_threads(split > 1), 1, 1);
         q.dynamicSmemBytes = Cfg::SMEM_BYTES;
         cudaLaunchAttribute qa[1];
         qa[0].id = cudaLaunchAttributeClusterDimension;
@@ -1045,7 +1038,7 @@ nm_status launch_ffn(const FfnMaps &maps, FfnArgs p, const FfnPlan &plan, cudaSt
     p.tile_rows = plan.tile_rows;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * plan.split * plan.clusters), 1, 1);
-    cfg.blockDim = dim3(Cfg::THREADS, 1, 1);
+    cfg.blockDim = dim3(ffn_threads(plan.split > 1), 1, 1);
     cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
