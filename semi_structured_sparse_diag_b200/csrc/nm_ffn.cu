@@ -898,6 +898,191 @@ __global__ void __launch_bounds__(SHRINK_THREADS)
     if (!p.first) grid_dep_wait();  // completes after the staging kernel, for the product's sake
 }
 
+// The same for tiles whose slots hold many tokens (prompts): V of a whole token
+// tile by tcgen05.mma, M = 128 tokens (twice for tiles wider than that), N = the
+// rank block, X and A through TMA.  Rows of other adapters' tokens are computed
+// and dropped.  A cluster of SHRINK_PARTS blocks splits K; warp 0 loads, warp 1
+// issues, then all four move the fp32 sums to shared memory, and block i adds
+// the parts for its share of the tokens.  (mma.sync from registers, as above,
+// ran into the L1 cache's rate, eight lines to a load: 92 us for 8192 tokens of
+// 4096 columns, rank 64.)
+struct WideShrink {
+    static constexpr int STAGES = 2, X_BYTES = 2 * 128 * 128, A_BYTES = SHRINK_RANKS * 128;
+    static constexpr int STAGE_BYTES = X_BYTES + A_BYTES;
+    static constexpr int SUM_LD = SHRINK_RANKS + 4;  // floats per token: 16-byte pieces without bank conflicts
+    // the sums lie over the stages, so that two blocks fit on an SM
+    static constexpr int SMEM_BYTES = STAGES * STAGE_BYTES + static_cast<int>(sizeof(TilePlan)) + 256 + 1024;
+    static_assert(256 * SUM_LD * 4 <= STAGES * STAGE_BYTES && 2 * (SMEM_BYTES + 1024) <= 233472, "shared memory");
+};
+
+__global__ void __launch_bounds__(SHRINK_THREADS, 2)
+    k_lora_shrink_wide(const __grid_constant__ ShrinkArgs p, const __grid_constant__ CUtensorMap tmx,
+                       const __grid_constant__ CUtensorMap tma) {
+    using C = WideShrink;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    float *sums = reinterpret_cast<float *>(smem);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::STAGES * C::STAGE_BYTES);
+    uint64_t *full = bars, *empty = bars + C::STAGES, *done = bars + 2 * C::STAGES;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+    TilePlan &plan = *reinterpret_cast<TilePlan *>(bars + 16);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int part = static_cast<int>(cluster_ctarank());
+    const int64_t tile = blockIdx.y, t0 = tile * p.bn;
+    const int rk = static_cast<int>(blockIdx.z % p.rb) * SHRINK_RANKS;
+    const int lanes_z = gridDim.z / p.rb;
+    const int nr = p.r - rk < SHRINK_RANKS ? p.r - rk : SHRINK_RANKS;
+    const int nkb = static_cast<int>((p.K + 63) / 64);
+    const int kb0 = nkb * part / SHRINK_PARTS, kb1 = nkb * (part + 1) / SHRINK_PARTS;
+    const bool two = p.bn > 128;
+    if (p.first) grid_dep_wait();
+    grid_dep_launch();
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        mbar_init(done, 1);
+        fence_barrier_init();
+        prefetch_tmap(&tmx);
+        prefetch_tmap(&tma);
+    }
+    if (warp == 1) {
+        tmem_alloc(tmem_slot, 128);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    const bool bad = plan_tile(p, tile, plan);  // synchronises the block
+    tc_fence_after();
+    if (bad) raise_error(ERRBIT_DEVICE);
+    const uint32_t tmem_base = *tmem_slot;
+    const int cnt = plan.cnt;
+    const int64_t base = plan.base;
+    if (blockIdx.x == 0 && blockIdx.z == 0) {  // what the product reads
+        for (int k = threadIdx.x; k < cnt; k += SHRINK_THREADS) p.slot_adapter[base + k] = plan.adapter[k];
+        if (threadIdx.x == 0) {
+            p.tile_cnt[tile] = cnt;
+            p.tile_base[tile] = static_cast<int32_t>(base);
+        }
+    }
+    int s = 0, it = 0;
+    uint32_t ph = 0, dph = 0;
+    bool ok = true;
+    for (int j = blockIdx.z / p.rb; j < cnt; j += lanes_z) {  // the same in every block of the cluster
+        const int32_t ad = plan.adapter[j];
+        if (warp == 0) {
+            const bool lead = elect_one() != 0u;
+            int ls = s, li = it;
+            uint32_t lp = ph;
+            for (int kb = kb0; kb < kb1 && ok; ++kb, ++li) {
+                if (li >= C::STAGES && !mbar_wait(&empty[ls], lp ^ 1u)) ok = false;
+                if (ok && lead) {
+                    uint8_t *st = smem + ls * C::STAGE_BYTES;
+                    mbar_arrive_expect_tx(&full[ls], static_cast<uint32_t>((two ? C::X_BYTES : C::X_BYTES / 2) + C::A_BYTES));
+                    tma_load_2d(st, &tmx, &full[ls], kb * 64, static_cast<int32_t>(t0));
+                    if (two) tma_load_2d(st + C::X_BYTES / 2, &tmx, &full[ls], kb * 64, static_cast<int32_t>(t0 + 128));
+                    tma_load_3d(st + C::X_BYTES, &tma, &full[ls], kb * 64, rk, ad);
+                }
+                __syncwarp();
+                if (++ls == C::STAGES) { ls = 0; lp ^= 1u; }
+            }
+        } else if (warp == 1) {
+            const bool lead = elect_one() != 0u;
+            const uint32_t idesc = make_idesc_bf16(128, static_cast<uint32_t>((nr + 15) / 16 * 16), false, 0);
+            const uint64_t xd = make_sdesc(smem_u32(smem), 16, 1024, 2), yd = make_sdesc(smem_u32(smem) + C::X_BYTES / 2, 16, 1024, 2);
+            const uint64_t ad0 = make_sdesc(smem_u32(smem) + C::X_BYTES, 16, 1024, 2);
+            int ls = s;
+            uint32_t lp = ph;
+            for (int kb = kb0; kb < kb1 && ok; ++kb) {
+                if (!mbar_wait(&full[ls], lp)) ok = false;
+                tc_fence_after();
+                if (ok && lead) {
+                    const uint64_t so = static_cast<uint64_t>(static_cast<uint32_t>(ls) * (C::STAGE_BYTES >> 4));
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t acc = kb > kb0 || k > 0 ? 1u : 0u;
+                        mma_bf16(tmem_base, xd + so + 2 * k, ad0 + so + 2 * k, idesc, acc);
+                        if (two) mma_bf16(tmem_base + SHRINK_RANKS, yd + so + 2 * k, ad0 + so + 2 * k, idesc, acc);
+                    }
+                    mma_commit(&empty[ls]);
+                    if (kb + 1 == kb1) mma_commit(done);
+                }
+                __syncwarp();
+                if (++ls == C::STAGES) { ls = 0; lp ^= 1u; }
+            }
+        }
+        const int n = kb1 - kb0;  // every warp keeps count of the stages
+        it += n;
+        s += n % C::STAGES;
+        if (s >= C::STAGES) s -= C::STAGES;
+        ph = static_cast<uint32_t>((it / C::STAGES) & 1);
+        if (n > 0) {
+            if (!mbar_wait(done, dph)) ok = false;
+            dph ^= 1u;
+        }
+        tc_fence_after();
+        // sums [token][rank]: warp = 32 tokens of each half
+        for (int half = 0; half < (two ? 2 : 1); ++half) {
+            float *row = sums + (half * 128 + warp * 32 + lane) * C::SUM_LD;
+            for (int c = 0; c < nr; c += 16) {
+                uint32_t v[16];
+                tmem_ld_32x32b_x16(tmem_base + (static_cast<uint32_t>(warp * 32) << 16) + half * SHRINK_RANKS + c, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<float4 *>(row + c + 4 * i) =
+                        n > 0 ? make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]),
+                                            __uint_as_float(v[4 * i + 2]), __uint_as_float(v[4 * i + 3]))
+                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            }
+        }
+        tc_fence_before();
+        cluster_sync_all();
+        tc_fence_after();
+        const float sc = __ldg(p.scale + ad);
+        uint16_t *vslot = p.V + (base + j) * p.bn * static_cast<int64_t>(p.r) + rk;
+        const int quads = nr / 4;
+        for (int e = threadIdx.x; e < (p.bn + SHRINK_PARTS - 1 - part) / SHRINK_PARTS * quads; e += SHRINK_THREADS) {
+            const int i = e / quads, c = 4 * (e - i * quads), tok = i * SHRINK_PARTS + part;
+            uint2 out = make_uint2(0u, 0u);
+            if (plan.slot[tok] == j) {
+                const uint32_t at = smem_u32(sums + tok * C::SUM_LD + c);
+                float4 v[SHRINK_PARTS];
+#pragma unroll
+                for (int w = 0; w < SHRINK_PARTS; ++w) {
+                    uint32_t from;
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(at), "r"(w));
+                    v[w] = ld_dsmem_f32x4(from);
+                }
+                float4 f = v[0];
+#pragma unroll
+                for (int w = 1; w < SHRINK_PARTS; ++w) {
+                    f.x += v[w].x;
+                    f.y += v[w].y;
+                    f.z += v[w].z;
+                    f.w += v[w].w;
+                }
+                out = make_uint2(pack_bf16x2(f.x * sc, f.y * sc), pack_bf16x2(f.z * sc, f.w * sc));
+            }
+            *reinterpret_cast<uint2 *>(vslot + static_cast<int64_t>(tok) * p.r + c) = out;
+        }
+        fence_proxy_async_smem();
+        cluster_sync_all();  // the sums have been read; TMA may write there again
+    }
+    // a wait that ran out: let copies already issued land before exiting
+    if (!ok && warp == 0)
+        for (int q = it > C::STAGES ? it - C::STAGES : 0; q < it; ++q)
+            mbar_wait(&full[q % C::STAGES], static_cast<uint32_t>((q / C::STAGES) & 1));
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem_base, 128);
+    }
+    if (!p.first) grid_dep_wait();  // completes after the staging kernel, for the product's sake
+}
+
 }  // namespace nm
 
 // ===========================================================================
@@ -1056,8 +1241,8 @@ nm_status launch_ffn(const FfnMaps &maps, FfnArgs p, const FfnPlan &plan, cudaSt
     return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
 }
 
-template <int NN>
-nm_status launch_shrink(const ShrinkArgs &p, dim3 grid, cudaStream_t s) {
+template <class Kernel, class... Args>
+nm_status launch_shrink(Kernel kernel, dim3 grid, int smem, cudaStream_t s, const Args &...args) {
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = SHRINK_PARTS;
@@ -1068,10 +1253,11 @@ nm_status launch_shrink(const ShrinkArgs &p, dim3 grid, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(SHRINK_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    if (cudaLaunchKernelEx(&cfg, k_lora_shrink<NN>, p) != cudaSuccess) return NM_ERR_CUDA;
+    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) return NM_ERR_CUDA;
     return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
 }
 
@@ -1294,15 +1480,31 @@ extern "C" nm_status nm_sparse_gemm_lora(const uint16_t *X, int64_t T, int64_t K
         a.tile_base = tile_base;
         a.slot_adapter = slot_adapter;
         a.V = V;
+        // prompts: at least 16 tokens a request on average, and enough of them that
+        // the wide kernel's start (some 8 us) is less than what the L1 cache costs
+        // the other (8192 tokens: TODO; 777: 12.5 us against 15.8)
+        if (T >= 16 * requests && T >= 1024) {
+            CUtensorMap tx, ta;
+            if (!set_smem_attr<k_lora_shrink_wide>(WideShrink::SMEM_BYTES) ||
+                !make_tmap_bf16(&tx, X, T, K, ldx, 64, 128, true) ||
+                !make_tmap_bf16_3d(&ta, A, adapters, r, K, lda, sda, 64, SHRINK_RANKS))
+                return NM_ERR_CUDA;
+            const dim3 grid(static_cast<unsigned>(SHRINK_PARTS), static_cast<unsigned>(tiles),
+                            static_cast<unsigned>((cap < 2 ? cap : 2) * p.rb));
+            st = launch_shrink(k_lora_shrink_wide, grid, WideShrink::SMEM_BYTES, s, a, tx, ta);
+            if (st != NM_OK) return st;
+            return m == 8 ? launch_ffn<PMODE_SP68T, OP_LORA>(maps, p, plan, s)
+                          : launch_ffn<PMODE_SP24, OP_LORA>(maps, p, plan, s);
+        }
         // slots side by side until the blocks fill the device some eight times over
         int64_t lanes = 8 * sm_count() / (tiles * SHRINK_PARTS) + 1;
         if (lanes > cap) lanes = cap;
         const dim3 grid(static_cast<unsigned>(SHRINK_PARTS), static_cast<unsigned>(tiles),
                         static_cast<unsigned>(lanes * p.rb));
-        st = r <= 8    ? launch_shrink<1>(a, grid, s)
-             : r <= 16 ? launch_shrink<2>(a, grid, s)
-             : r <= 32 ? launch_shrink<4>(a, grid, s)
-                       : launch_shrink<8>(a, grid, s);
+        st = r <= 8    ? launch_shrink(k_lora_shrink<1>, grid, 0, s, a)
+             : r <= 16 ? launch_shrink(k_lora_shrink<2>, grid, 0, s, a)
+             : r <= 32 ? launch_shrink(k_lora_shrink<4>, grid, 0, s, a)
+                       : launch_shrink(k_lora_shrink<8>, grid, 0, s, a);
         if (st != NM_OK) return st;
     }
     return m == 8 ? launch_ffn<PMODE_SP68T, OP_LORA>(maps, p, plan, s)

@@ -76,6 +76,12 @@ CASES = {
     "rank 256": (50, 256, 90, 10, 256, 2, [0, 25, 50], [1, 0]),
     "rank 72, 8:10": (260, 600, 1030, 10, 72, 4, [0, 240, 260], [3, 2]),
     "one request over many tiles": (1100, 300, 200, 4, 32, 2, [0, 1100], [1]),
+    "short requests of two adapters, rank 128": (230, 300, 333, 4, 128, 2, [min(230, 11 * i) for i in range(21)] + [230],
+                                                 [i % 2 for i in range(21)]),
+    "short requests, rank 40, several tiles": (900, 520, 1000, 8, 40, 7, list(range(0, 901, 10)), [(5 * i) % 8 - 1 for i in range(90)]),
+    "prompts, rank 128, 8:10": (1500, 264, 515, 10, 128, 3, [7, 400, 400, 900, 1301, 1490], [2, 0, -1, 1, 2]),
+    "prompts, rank 8": (2000, 300, 40, 4, 8, 2, [0, 1000, 1010, 2000], [1, 0, 1]),
+    "prompts, rank 72, 6:8": (1030, 520, 1030, 8, 72, 5, [0, 100, 330, 331, 1030], [4, 2, 0, 4]),
     "many short requests over tiles": (600, 256, 128, 8, 8, 200, list(range(0, 601, 3)), [(3 * i) % 200 for i in range(200)]),
 }
 
