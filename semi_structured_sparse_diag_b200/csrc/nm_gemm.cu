@@ -994,8 +994,11 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
                 // nothing; after one wait times out the rest are not waited for
                 bool got = true;
                 for (int64_t cc = cluster + 1; cc <= last_contrib && got; ++cc)
-                    if ((cc + 1) * total / nclusters > cc * total / nclusters)
-                        got = sk_wait_flag(flags + (cc * 2 + rank) * 8 + we, seq);
+                    if ((cc + 1) * total / nclusters > cc * total / nclusters) {
+                        uint64_t *fl = flags + (cc * 2 + rank) * 8 + we;
+                        got = sk_wait_flag(fl, seq);
+                        sk_clear_flag(fl, lane, got);
+                    }
             }
             uint32_t packed[64];
 #pragma unroll
@@ -1529,8 +1532,11 @@ __global__ void __launch_bounds__(WideCfg::THREADS, 1)
                 for (int64_t base = cluster + 1; base <= last_contrib && got; base += 32) {
                     const int64_t cc = base + lane;
                     bool mine = true;
-                    if (cc <= last_contrib && (all_work || has_work(cc)))
-                        mine = sk_wait_flag(flags + (cc * 2 + rank) * 8 + we, seq);
+                    if (cc <= last_contrib && (all_work || has_work(cc))) {
+                        uint64_t *fl = flags + (cc * 2 + rank) * 8 + we;
+                        mine = sk_wait_flag(fl, seq);
+                        if (mine) *static_cast<volatile uint64_t *>(fl) = 0;
+                    }
                     got = __all_sync(0xffffffffu, mine);
                 }
 #pragma unroll 1

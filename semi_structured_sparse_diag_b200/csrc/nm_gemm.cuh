@@ -144,6 +144,14 @@ __device__ __forceinline__ bool sk_wait_flag(const uint64_t *p, uint64_t seq) {
     }
 }
 
+// A flag has one reader, which clears it once seen: the replay of a captured
+// launch carries the same sequence number, and must not take the partial sums
+// of the replay before it for its own.  (Every lane has polled the flag.)
+__device__ __forceinline__ void sk_clear_flag(uint64_t *p, int lane, bool seen) {
+    __syncwarp();
+    if (lane == 0 && seen) *static_cast<volatile uint64_t *>(p) = 0;
+}
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
