@@ -461,6 +461,18 @@ def _matrix(t, name, shape):
         raise NMError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
 
 
+def _row_stride(t):
+    """Row stride of a matrix; a single row has none of its own."""
+    return t.stride(0) if t.shape[0] > 1 else (t.shape[1] + 7) // 8 * 8
+
+
+def _two_d(t, name):
+    _bf16(t, name)
+    if t.dim() != 2:
+        raise NMError(f"{name} must be a matrix, got {list(t.shape)}")
+    return t.shape
+
+
 def _one_device(dev, *tensors):
     """Every tensor on device `dev`, and that the current one: the library launches
     on the current device."""
@@ -526,8 +538,7 @@ def sparse_glu(X, packed_gate, packed_up, R, m, act="silu", save=False, H=None, 
     """H = act(X Wg^T) * (X Wu^T), both projections sparse, in one kernel; act is
     "silu", "gelu" (tanh form) or "relu2".  save=True returns (H, G, U) with
     G = X Wg^T and U = X Wu^T for sparse_glu_backward."""
-    _bf16(X, "X")
-    T, K = X.shape
+    T, K = _two_d(X, "X")
     a = _act(act)
     _operand(packed_gate, R, K, m, "packed_gate")
     _operand(packed_up, R, K, m, "packed_up")
@@ -542,10 +553,10 @@ def sparse_glu(X, packed_gate, packed_up, R, m, act="silu", save=False, H=None, 
             H = _out_rows(T, R, X.device)
         if save:
             G, U = _out_rows(T, R, X.device), _out_rows(T, R, X.device)
-            g, u, ld = G.data_ptr(), U.data_ptr(), G.stride(0)
+            g, u, ld = G.data_ptr(), U.data_ptr(), _row_stride(G)
         w, nbytes, ws = _scratch(ws, _ws_bytes("nm_sparse_glu_workspace_bytes", T, K, m), X)
-    st = load().nm_sparse_glu(X.data_ptr(), T, K, X.stride(0), packed_gate.data_ptr(), packed_up.data_ptr(), R, m, a,
-                              H.data_ptr(), H.stride(0), g, u, ld, w, nbytes, _raw(stream, dev))
+    st = load().nm_sparse_glu(X.data_ptr(), T, K, _row_stride(X), packed_gate.data_ptr(), packed_up.data_ptr(), R, m, a,
+                              H.data_ptr(), _row_stride(H), g, u, ld, w, nbytes, _raw(stream, dev))
     if st:
         _check(st, "nm_sparse_glu")
     return (H, G, U) if save else H
@@ -557,10 +568,8 @@ def sparse_glu_backward(dH, X, G, U, Wg, Wu, act="silu", mask_gate=None, mask_up
     Wu are the masked weights in dense form (sparse_densify).  Without masks
     dWg and dWu go straight through to every weight; with the masks of
     prune_compress (pattern width m) they are zero where the mask is."""
-    _bf16(X, "X")
-    _bf16(Wg, "Wg")
-    T, K = X.shape
-    R = Wg.shape[0]
+    T, K = _two_d(X, "X")
+    R = _two_d(Wg, "Wg")[0]
     a = _act(act)
     rows, weights = (T, R), (R, K)
     _matrix(dH, "dH", rows)
@@ -582,20 +591,21 @@ def sparse_glu_backward(dH, X, G, U, Wg, Wu, act="silu", mask_gate=None, mask_up
         mg, mu = mask_gate.data_ptr(), mask_up.data_ptr()
     dev = X.get_device()
     _one_device(dev, dH, G, U, Wg, Wu, mask_gate, mask_up, ws)
-    if G.stride(0) != U.stride(0) or Wg.stride(0) != Wu.stride(0):
+    ldgu, ldwgu = _row_stride(G), _row_stride(Wg)
+    if ldgu != _row_stride(U) or ldwgu != _row_stride(Wu):
         raise NMError("G and U, and Wg and Wu, must have the same row stride")
     dX = dWg = dWu = x = wg = wu = None
     ldx = ldw = 0
     with _on(stream):
         if need_dx:
             dX = _out_rows(T, K, X.device)
-            x, ldx = dX.data_ptr(), dX.stride(0)
+            x, ldx = dX.data_ptr(), _row_stride(dX)
         if need_dw:
             dWg, dWu = _out_rows(R, K, X.device), _out_rows(R, K, X.device)
-            wg, wu, ldw = dWg.data_ptr(), dWu.data_ptr(), dWg.stride(0)
+            wg, wu, ldw = dWg.data_ptr(), dWu.data_ptr(), _row_stride(dWg)
         w, nbytes, ws = _scratch(ws, _ws_bytes("nm_sparse_glu_backward_workspace_bytes", T, R), X)
-    st = load().nm_sparse_glu_backward(dH.data_ptr(), dH.stride(0), X.data_ptr(), T, K, X.stride(0), G.data_ptr(),
-                                       U.data_ptr(), G.stride(0), Wg.data_ptr(), Wu.data_ptr(), R, Wg.stride(0), a, mg,
+    st = load().nm_sparse_glu_backward(dH.data_ptr(), _row_stride(dH), X.data_ptr(), T, K, _row_stride(X), G.data_ptr(),
+                                       U.data_ptr(), ldgu, Wg.data_ptr(), Wu.data_ptr(), R, ldwgu, a, mg,
                                        mu, m or 0, x, ldx, wg, wu, ldw, w, nbytes, _raw(stream, dev))
     if st:
         _check(st, "nm_sparse_glu_backward")
@@ -620,7 +630,7 @@ def sparse_densify(vals, mask, R, K, n, m, W=None, stream=None):
     else:
         with _on(stream):
             W = _out_rows(R, K, vals.device)
-    _check(load().nm_sparse_densify(vals.data_ptr(), mask.data_ptr(), R, K, n, m, W.data_ptr(), W.stride(0),
+    _check(load().nm_sparse_densify(vals.data_ptr(), mask.data_ptr(), R, K, n, m, W.data_ptr(), _row_stride(W),
                                     _raw(stream, dev)), "nm_sparse_densify")
     return W
 
@@ -630,9 +640,8 @@ def sparse_gemm_lora(X, packed, R, m, A, B, scale, indptr, ids, Y=None, ws=None,
     i, scale[a] (X A[a]^T) B[a]^T with a = ids[i] (-1: no adapter).  A
     [adapters x r x K], B [adapters x R x r] bf16, scale fp32 [adapters],
     indptr int32 [requests + 1], ids int32 [requests], all on the device."""
-    _bf16(X, "X")
+    T, K = _two_d(X, "X")
     _bf16(A, "A")
-    T, K = X.shape
     if A.dim() != 3:
         raise NMError("A must be [adapters x r x K]")
     n, r, _ = A.shape
@@ -659,9 +668,11 @@ def sparse_gemm_lora(X, packed, R, m, A, B, scale, indptr, ids, Y=None, ws=None,
             Y = _out_rows(T, R, X.device)
         w, nbytes, ws = _scratch(ws, need, X)
     sa, sb = A.stride(), B.stride()
-    st = load().nm_sparse_gemm_lora(X.data_ptr(), T, K, X.stride(0), packed.data_ptr(), R, m, A.data_ptr(), sa[1],
-                                    sa[0], B.data_ptr(), sb[1], sb[0], scale.data_ptr(), n, r, indptr.data_ptr(),
-                                    ids.data_ptr(), q, Y.data_ptr(), Y.stride(0), w, nbytes, _raw(stream, dev))
+    lda, ldb = sa[1], sb[1] if R > 1 else r
+    sda, sdb = (sa[0], sb[0]) if n > 1 else (r * lda, R * ldb)  # of one adapter there is no stride
+    st = load().nm_sparse_gemm_lora(X.data_ptr(), T, K, _row_stride(X), packed.data_ptr(), R, m, A.data_ptr(), lda, sda,
+                                    B.data_ptr(), ldb, sdb, scale.data_ptr(), n, r, indptr.data_ptr(),
+                                    ids.data_ptr(), q, Y.data_ptr(), _row_stride(Y), w, nbytes, _raw(stream, dev))
     if st:
         _check(st, "nm_sparse_gemm_lora")
     return Y
