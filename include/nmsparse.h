@@ -386,11 +386,18 @@ nm_status nm_dense_gemm(const uint16_t *X, int64_t T, int64_t K, int64_t ldx, co
  *         (the same R, K and m; m in {4, 6, 8, 10}).  They may be one buffer.
  *   G, U: [T x R] bf16 (row stride ldgu >= R), both or neither (NULL): rounded
  *         from the same fp32 sums, for nm_sparse_glu_backward.
- *   ws  : as for nm_sparse_gemm, with nm_sparse_glu_workspace_bytes(T, K, m):
- *         too small for the staged activations -> NM_ERR_WORKSPACE; without
- *         the rest (NULL for 2:4) whole tiles only.  Not to be shared by calls
- *         that may run at the same time.  A captured call may be replayed, and
- *         graphs that never run at the same time may share it.
+ *   ws  : nm_sparse_glu_workspace_bytes(T, K, m) bytes, 16-byte aligned: the
+ *         staged activations, as in nm_sparse_gemm (nothing for 2:4: NULL);
+ *         smaller -> NM_ERR_WORKSPACE.  Not to be shared by calls that may run at
+ *         the same time.  A captured call may be replayed, and graphs that never
+ *         run at the same time may share it.
+ *   Scheduling: tiles of 256 features x up to 240 tokens over CTA pairs; when
+ *         they do not fill the device, narrower tiles, or up to eight pairs of a
+ *         thread-block cluster that split a tile's K' blocks and add their fp32
+ *         sums through distributed shared memory, always in the same order:
+ *         results are deterministic for a given device and schedule.
+ *         nm_gemm_set_schedule: 1 never splits, 2 always; its cluster count
+ *         bounds the clusters.
  * Any T >= 1.  Infinities and NaN of the sums pass through the formulas.     */
 enum { NM_ACT_SILU = 0, NM_ACT_GELU = 1, NM_ACT_RELU2 = 2 };
 size_t nm_sparse_glu_workspace_bytes(int64_t T, int64_t K, int m);
@@ -414,7 +421,9 @@ nm_status nm_sparse_glu(const uint16_t *X, int64_t T, int64_t K, int64_t ldx, co
  *            dWg NULL: X unused).
  *   ws  : nm_sparse_glu_backward_workspace_bytes(T, R) bytes, 16-byte aligned
  *         (dG and dU).  Not to be shared by calls that may run at the same time.
- * Sums run in a fixed order: repeated calls agree bit for bit.               */
+ * Two launches: dG and dU, then all three products.  Sums run in a fixed order:
+ * repeated calls agree bit for bit.  With few tokens dX's contraction is split
+ * over the pairs of a cluster, as above.                                     */
 size_t nm_sparse_glu_backward_workspace_bytes(int64_t T, int64_t R);
 nm_status nm_sparse_glu_backward(const uint16_t *dH, int64_t lddh, const uint16_t *X, int64_t T, int64_t K,
                                  int64_t ldx, const uint16_t *G, const uint16_t *U, int64_t ldgu,
@@ -448,6 +457,11 @@ nm_status nm_sparse_densify(const uint16_t *vals, const uint32_t *mask, int64_t 
  *       A list that is not ascending within [0, T], or an id outside [-1,
  *       adapters), sets NM_ERR_DEVICE in the device error word; the outputs are
  *       then unspecified, and no memory outside the arguments is touched.
+ *   Two launches (three for 4:6, 6:8, 8:10, whose activations are staged as in
+ *       nm_sparse_gemm): V, then the product, scheduled as nm_sparse_glu's with
+ *       tiles of 256 or 512 rows.  V costs one pass over X per adapter of a tile
+ *       of up to 240 tokens, the product one dense block of 64 ranks (four
+ *       adapters of rank <= 16, two of rank <= 32) per tile.
  *   ws : nm_sparse_gemm_lora_workspace_bytes(...) bytes, 16-byte aligned,
  *       required.  Not to be shared by calls that may run at the same time.  A
  *       captured call may be replayed (with other contents of every array), and

@@ -18,6 +18,13 @@
 //            accumulators, where V_a holds scale[a] X A[a]^T of that adapter's
 //            tokens and zero in the other rows (k_lora_shrink).  The adapters'
 //            share so joins the projection's in fp32 and Y is written once.
+// Where the time goes (device time, 11008 x 4096 2:4 projections): one token
+// through gate and up 20.0 us, 101 MB of operands at 5.1 TB/s (78% of a measured
+// copy): HBM, and some 5 us of start and tail.  8192 tokens with G and U kept
+// 720 us in a long run, which the power cap bounds (1.4 GHz); 494 us at
+// 1965 MHz, the tensor pipe 69% active: 15 us of products and 5 us of epilogue a
+// tile, the latter bound by all SMs' stores at once.  8192 tokens with rank 64
+// adapters 370 us, of which the product 296 and V 41.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -482,9 +489,11 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
                 // the layout of a matrix fragment, transposed by stmatrix on the way to
                 // the warp's 1 KB of shared memory ([token][32 rows], 16-byte pieces
                 // swizzled against bank conflicts), and out as 64 bytes a token.  (Two-byte
-                // stores straight from registers, a row to each lane, took as long as the
-                // tile's products: 820 us for 8192 tokens against TODO.)  The accumulators
-                // are released once the last chunk is in registers.
+                // stores straight from registers, a row to each lane, took 14 us a tile where
+                // the products take 15 and this takes 5: 820 us against 720 for 8192
+                // tokens of the 7B-shaped projections with G and U kept, 494 against 524
+                // with eight warps at 1965 MHz.)  The accumulators are released once the
+                // last chunk is in registers.
                 const int64_t row0 = mt * tile_rows + acc0 * 256 + rank * 128 + q * 32;
                 const uint32_t buf = smem_u32(smem) + C::OFF_OUT + static_cast<uint32_t>(warp - 4) * 1024u;
                 const int bi = lane >> 3, st_tok = (lane & 7) + 8 * (bi >> 1);
@@ -904,8 +913,10 @@ __global__ void __launch_bounds__(SHRINK_THREADS)
 // and dropped.  A cluster of SHRINK_PARTS blocks splits K; warp 0 loads, warp 1
 // issues, then all four move the fp32 sums to shared memory, and block i adds
 // the parts for its share of the tokens.  (mma.sync from registers, as above,
-// ran into the L1 cache's rate, eight lines to a load: 92 us for 8192 tokens of
-// 4096 columns, rank 64.)
+// runs into the L1 cache's rate, eight lines to a load: 92 us for 8192 tokens of
+// 4096 columns, rank 64; this 41 us, of which 11 are the reading of X.  Bound by
+// the start and the exchange of short blocks; two blocks an SM hide part of it,
+// one took 57 us.)
 struct WideShrink {
     static constexpr int STAGES = 2, X_BYTES = 2 * 128 * 128, A_BYTES = SHRINK_RANKS * 128;
     static constexpr int STAGE_BYTES = X_BYTES + A_BYTES;
@@ -1482,7 +1493,8 @@ extern "C" nm_status nm_sparse_gemm_lora(const uint16_t *X, int64_t T, int64_t K
         a.V = V;
         // prompts: at least 16 tokens a request on average, and enough of them that
         // the wide kernel's start (some 8 us) is less than what the L1 cache costs
-        // the other (8192 tokens: TODO; 777: 12.5 us against 15.8)
+        // the other (8192 tokens, rank 64: 41 us against 92; 777, rank 8: 15.8
+        // against 12.5)
         if (T >= 16 * requests && T >= 1024) {
             CUtensorMap tx, ta;
             if (!set_smem_attr<k_lora_shrink_wide>(WideShrink::SMEM_BYTES) ||
