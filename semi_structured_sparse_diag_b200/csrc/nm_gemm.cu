@@ -1674,6 +1674,9 @@ constexpr int GATHER_TOKENS = 4;
 __global__ void __launch_bounds__(256)
     k_gather_mid(const uint16_t *__restrict__ X, int64_t T, int64_t K, int64_t ldx, int64_t G,
                  uint16_t *__restrict__ Xmid, int64_t ldm) {
+    // a programmatic dependent itself: set up while the kernel before ends; the GEMM
+    // may start once that one is done, since it loads X and the weights early
+    grid_dep_wait();
     grid_dep_launch();
     const int64_t t0 = (blockIdx.y + static_cast<int64_t>(blockIdx.z) * 65535) * GATHER_TOKENS;
     const int64_t h = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;  // group pair
@@ -1729,8 +1732,7 @@ nm_status nm::launch_gather_mid(const uint16_t *X, int64_t T, int64_t K, int64_t
     const int64_t runs = (T + GATHER_TOKENS - 1) / GATHER_TOKENS;
     dim3 grid(static_cast<unsigned>((pairs + 255) / 256), static_cast<unsigned>(runs < 65535 ? runs : 65535),
               static_cast<unsigned>((runs + 65534) / 65535));
-    k_gather_mid<<<grid, 256, 0, s>>>(X, T, K, ldx, G, Xmid, ldm);
-    return cudaGetLastError() == cudaSuccess ? NM_OK : NM_ERR_CUDA;
+    return launch_dependent(k_gather_mid, grid, 256, s, X, T, K, ldx, G, Xmid, ldm) ? NM_OK : NM_ERR_CUDA;
 }
 
 namespace {

@@ -50,6 +50,7 @@ __global__ void __launch_bounds__(256)
     k_glu_grad(const uint16_t *__restrict__ dH, int64_t lddh, const uint16_t *__restrict__ G,
                const uint16_t *__restrict__ U, int64_t ldgu, int64_t T, int64_t R, int act,
                uint16_t *__restrict__ dG, uint16_t *__restrict__ dU, int64_t ldd) {
+    grid_dep_wait();
     grid_dep_launch();
     const int64_t t = blockIdx.y + static_cast<int64_t>(blockIdx.z) * 65535;
     const int64_t c = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * 8;
@@ -235,6 +236,7 @@ __global__ void __launch_bounds__(GradCfg::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
     grid_dep_wait();
+    grid_dep_launch();  // the stream's next kernel may set itself up
 
     if (warp == 0) {
         // ---------------------------------------------------------- producer
@@ -674,8 +676,7 @@ extern "C" nm_status nm_sparse_glu_backward(const uint16_t *dH, int64_t lddh, co
     const int64_t chunks = (R + 7) / 8;
     dim3 grid(static_cast<unsigned>((chunks + 255) / 256), static_cast<unsigned>(T < 65535 ? T : 65535),
               static_cast<unsigned>((T + 65534) / 65535));
-    k_glu_grad<<<grid, 256, 0, s>>>(dH, lddh, G, U, ldgu, T, R, act, dG, dU, ldd);
-    if (cudaGetLastError() != cudaSuccess) return NM_ERR_CUDA;
+    if (!launch_dependent(k_glu_grad, grid, 256, s, dH, lddh, G, U, ldgu, T, R, act, dG, dU, ldd)) return NM_ERR_CUDA;
     return launch_grad(maps, p, s);
 }
 

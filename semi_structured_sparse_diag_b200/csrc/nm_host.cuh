@@ -87,4 +87,21 @@ inline bool set_smem_attr(int bytes) {
     return true;
 }
 
+// launches a kernel that calls grid_dep_wait before it touches memory, so that
+// its start overlaps the end of the kernel before it in the stream
+template <class... Params, class... Args>
+inline bool launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned threads, cudaStream_t s, Args... args) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<Params>(args)...) == cudaSuccess &&
+           cudaGetLastError() == cudaSuccess;
+}
+
 }  // namespace nm

@@ -1198,6 +1198,8 @@ __global__ void __launch_bounds__(256)
 __global__ void __launch_bounds__(256)
     k_lift(const uint16_t *__restrict__ X, int64_t T, int64_t K, int64_t ldx, int m, int64_t G,
            uint16_t *__restrict__ XL, int64_t ldxl) {
+    grid_dep_wait();
+    grid_dep_launch();
     const int Ns = m / 2, nwin = Ns - 1;
     const int64_t g = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
     const int64_t t = blockIdx.y;
@@ -1801,8 +1803,7 @@ extern "C" nm_status lift_activations(const uint16_t *X, int64_t T, int64_t K, i
     if (!aligned16(X) || !aligned16(XL) || (ldx % 8) != 0 || (ldxl % 8) != 0) return NM_ERR_ALIGN;
     if (T > 65535) return NM_ERR_SHAPE;
     dim3 grid(static_cast<unsigned>((G + 255) / 256), static_cast<unsigned>(T));
-    k_lift<<<grid, 256, 0, as_stream(stream)>>>(X, T, K, ldx, m, G, XL, ldxl);
-    return launch_status();
+    return launch_dependent(k_lift, grid, 256, as_stream(stream), X, T, K, ldx, m, G, XL, ldxl) ? NM_OK : NM_ERR_CUDA;
 }
 
 extern "C" size_t nm_ternary_workspace_bytes(int64_t R) {
