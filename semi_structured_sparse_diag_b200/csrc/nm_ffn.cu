@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
 // each tile or request border starts at most one new pair, so that numbering
 // leaves every tile room and needs requests + tiles slots in all.
 //
-// k_lora_shrink, one (tile, slot, rank block of <= 64) per cluster of
+// k_lora_shrink, one (tile, slot, rank block of <= 64) per cluster of up to
 // SHRINK_PARTS blocks that split K.  Every block first works out its tile's
 // slots (one pass over the list, a hash of the adapters; about a microsecond,
 // less than a kernel of its own would take to start), then, for its slots,
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
 // added in a fixed order, through shared and distributed shared memory.
 // ---------------------------------------------------------------------------
 constexpr int SHRINK_GROUP = 32, SHRINK_RANKS = 64, SHRINK_WARPS = 4, SHRINK_THREADS = 32 * SHRINK_WARPS;
-constexpr int SHRINK_PARTS = 8;      // blocks of a cluster
+constexpr int SHRINK_PARTS = 8;      // blocks of a cluster, at most
 constexpr int SHRINK_HASH = 512;     // more than twice the tokens of a tile
 
 // eight bf16 of a row from column k on, zero past K
@@ -627,6 +627,7 @@ struct ShrinkArgs {
     int32_t requests, adapters;
     int r, rb, bn, cap, by_cap;
     int first;  // the call's first kernel (else it follows the staging kernel)
+    int parts;  // blocks of a cluster
     int32_t *tile_cnt, *tile_base, *slot_adapter;
     uint16_t *V;
 };
@@ -750,7 +751,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS)
     if (p.first) grid_dep_wait();
     grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tg = lane & 3;
-    const int part = static_cast<int>(cluster_ctarank());
+    const int part = static_cast<int>(cluster_ctarank()), parts = p.parts;
     const int64_t tile = blockIdx.y, t0 = tile * p.bn;
     const int rk = static_cast<int>(blockIdx.z % p.rb) * SHRINK_RANKS;
     const int lanes_z = gridDim.z / p.rb;
@@ -786,7 +787,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS)
                 for (int w = 0; w < u * SHRINK_WARPS + warp; ++w) at += plan.warp_cnt[w];
                 plan.list[at] = threadIdx.x + u * SHRINK_THREADS;
             }
-        for (int e = part * SHRINK_THREADS + threadIdx.x; e < p.bn * nn; e += SHRINK_PARTS * SHRINK_THREADS) {
+        for (int e = part * SHRINK_THREADS + threadIdx.x; e < p.bn * nn; e += parts * SHRINK_THREADS) {
             const int tok = e / nn;
             if (plan.slot[tok] != j)
                 *reinterpret_cast<uint4 *>(vslot + static_cast<int64_t>(tok) * p.r + (e - tok * nn) * 8) =
@@ -819,7 +820,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS)
 #pragma unroll
             for (int c = 0; c < NN; ++c) ar[c] = arow + static_cast<int64_t>(c < nn ? c * 8 : 0) * p.lda + tg * 8;
             const bool hi = g0 + 16 < n;  // more than 16 tokens: the second m-tile
-            const int stride = 32 * SHRINK_PARTS * (one ? SHRINK_WARPS : 1);
+            const int stride = 32 * parts * (one ? SHRINK_WARPS : 1);
             const int K = static_cast<int>(p.K), whole = K & ~31;
             int k = 32 * (one ? part * SHRINK_WARPS + warp : part);
             if (g0 >= n) k = K;
@@ -879,25 +880,26 @@ __global__ void __launch_bounds__(SHRINK_THREADS)
                 }
             }
             cluster_sync_all();
-            // the round's tokens, one in SHRINK_PARTS to each block, added over the blocks
+            // the round's tokens, one in `parts` to each block, added over the blocks
             const int left = n - first < groups * SHRINK_GROUP ? n - first : groups * SHRINK_GROUP;
             const int half = nr / 2;
-            for (int e = threadIdx.x; e < (left + SHRINK_PARTS - 1 - part) / SHRINK_PARTS * half; e += SHRINK_THREADS) {
-                const int i = e / half, c = 2 * (e - i * half), tok = i * SHRINK_PARTS + part;
+            for (int e = threadIdx.x; e < (left + parts - 1 - part) / parts * half; e += SHRINK_THREADS) {
+                const int i = e / half, c = 2 * (e - i * half), tok = i * parts + part;
                 const uint32_t at = smem_u32(&red[0][0][0]) + static_cast<uint32_t>((tok * NR + c) * 4);
                 float v0[SHRINK_PARTS], v1[SHRINK_PARTS], s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
                 for (int w = 0; w < SHRINK_PARTS; ++w) {
                     uint32_t from;
-                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(at), "r"(w));
-                    v0[w] = ld_dsmem_f32(from);
-                    v1[w] = ld_dsmem_f32(from + 4);
+                    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(at), "r"(w < parts ? w : part));
+                    v0[w] = w < parts ? ld_dsmem_f32(from) : 0.0f;
+                    v1[w] = w < parts ? ld_dsmem_f32(from + 4) : 0.0f;
                 }
 #pragma unroll
-                for (int w = 0; w < SHRINK_PARTS; ++w) {
-                    s0 += v0[w];
-                    s1 += v1[w];
-                }
+                for (int w = 0; w < SHRINK_PARTS; ++w)
+                    if (w < parts) {
+                        s0 += v0[w];
+                        s1 += v1[w];
+                    }
                 *reinterpret_cast<uint32_t *>(vslot + static_cast<int64_t>(plan.list[first + tok]) * p.r + c) =
                     pack_bf16x2(s0 * sc, s1 * sc);
             }
@@ -1253,10 +1255,10 @@ nm_status launch_ffn(const FfnMaps &maps, FfnArgs p, const FfnPlan &plan, cudaSt
 }
 
 template <class Kernel, class... Args>
-nm_status launch_shrink(Kernel kernel, dim3 grid, int smem, cudaStream_t s, const Args &...args) {
+nm_status launch_shrink(Kernel kernel, dim3 grid, int smem, cudaStream_t s, const Args &...args) {  // grid.x: the cluster
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = SHRINK_PARTS;
+    attr[0].val.clusterDim.x = grid.x;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1487,6 +1489,7 @@ extern "C" nm_status nm_sparse_gemm_lora(const uint16_t *X, int64_t T, int64_t K
         a.cap = static_cast<int>(cap);
         a.by_cap = by_cap;
         a.first = m == 4 ? 1 : 0;
+        a.parts = SHRINK_PARTS;
         a.tile_cnt = tile_cnt;
         a.tile_base = tile_base;
         a.slot_adapter = slot_adapter;
@@ -1508,11 +1511,14 @@ extern "C" nm_status nm_sparse_gemm_lora(const uint16_t *X, int64_t T, int64_t K
             return m == 8 ? launch_ffn<PMODE_SP68T, OP_LORA>(maps, p, plan, s)
                           : launch_ffn<PMODE_SP24, OP_LORA>(maps, p, plan, s);
         }
-        // slots side by side until the blocks fill the device some eight times over
-        int64_t lanes = 8 * sm_count() / (tiles * SHRINK_PARTS) + 1;
+        // all slots side by side, and K in as many parts as fit on the device then
+        // (three blocks an SM); more slots than that take turns
+        int64_t lanes = cap, at_once = 3 * sm_count() / (tiles * p.rb);
+        a.parts = SHRINK_PARTS;
+        while (a.parts > 2 && lanes * a.parts > at_once) a.parts /= 2;
+        if (lanes * a.parts > 2 * at_once) lanes = 2 * at_once / a.parts + 1;
         if (lanes > cap) lanes = cap;
-        const dim3 grid(static_cast<unsigned>(SHRINK_PARTS), static_cast<unsigned>(tiles),
-                        static_cast<unsigned>(lanes * p.rb));
+        const dim3 grid(static_cast<unsigned>(a.parts), static_cast<unsigned>(tiles), static_cast<unsigned>(lanes * p.rb));
         st = r <= 8    ? launch_shrink(k_lora_shrink<1>, grid, 0, s, a)
              : r <= 16 ? launch_shrink(k_lora_shrink<2>, grid, 0, s, a)
              : r <= 32 ? launch_shrink(k_lora_shrink<4>, grid, 0, s, a)

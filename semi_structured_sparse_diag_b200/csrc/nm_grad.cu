@@ -147,7 +147,8 @@ struct GradArgs {
 
 // The tiles of one pair, in order.  dX: the cluster's tile (SPLIT, at most one
 // each) or pair, pair + pairs, ..  dW: likewise, but where the last round of dX
-// leaves pairs out, those first take `extra` tiles each, about as much work.
+// leaves pairs out (out0 and up), those come first, and first take `extra` tiles
+// each, about as much work.
 struct GradIter {
     int64_t n_x, n_w, pairs, pair, out0, extra, jx, jw;
     __device__ GradIter(const GradArgs &p, int64_t cluster, int64_t part, int64_t clusters)
@@ -159,8 +160,11 @@ struct GradIter {
             out0 = n_x % pairs == 0 ? pairs : n_x % pairs;
             jx = pair;
         }
+        // in blocks of the contraction; with few tokens a tile of dW takes as long as
+        // its epilogue, some six blocks
         const int64_t bx = 2 * ((p.R + 63) / 64) / p.split, bw = (p.T + 63) / 64;
-        extra = n_x == 0 ? 0 : bx / bw;
+        const int64_t c = bw > 6 ? bw : 6;
+        extra = n_x == 0 ? 0 : (bx + c / 2) / c;
         if (extra * (pairs - out0) > n_w) extra = 0;
         split = p.split;
     }
@@ -180,7 +184,7 @@ struct GradIter {
         if (pair >= out0 && jw < extra)
             idx = (pair - out0) * extra + jw;
         else
-            idx = given + pair + (jw - (pair >= out0 ? extra : 0)) * pairs;
+            idx = given + (pair >= out0 ? pair - out0 : pair + pairs - out0) + (jw - (pair >= out0 ? extra : 0)) * pairs;
         ++jw;
         if (idx >= n_w) return false;
         src = idx >= n_w / 2 ? 1 : 0;
