@@ -421,7 +421,8 @@ nm_status nm_sparse_glu(const uint16_t *X, int64_t T, int64_t K, int64_t ldx, co
  *            dWg NULL: X unused).
  *   ws  : nm_sparse_glu_backward_workspace_bytes(T, R) bytes, 16-byte aligned
  *         (dG and dU).  Not to be shared by calls that may run at the same time.
- * Two launches: dG and dU, then all three products.  Sums run in a fixed order:
+ * Two launches: dG and dU, then all three products (dX apart when it is
+ * large).  Sums run in a fixed order:
  * repeated calls agree bit for bit.  With few tokens dX's contraction is split
  * over the pairs of a cluster, as above.                                     */
 size_t nm_sparse_glu_backward_workspace_bytes(int64_t T, int64_t R);
