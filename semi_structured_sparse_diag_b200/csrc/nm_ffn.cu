@@ -74,6 +74,7 @@ struct FfnArgs {
     int split;    // CTA pairs of a cluster that share a tile
     int sum_off;  // split > 1: where a CTA leaves its fp32 sums in shared memory
     int early;    // loads of X and the weights need not wait for the preceding kernel
+    int stream_out;  // outputs larger than L2 can keep: written to be evicted first
     uint16_t *Y, *G, *U;
     int64_t ldy, ldgu;
     int act;
@@ -144,6 +145,10 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
     const int64_t nkb = p.nkb, T = p.T;
     const int64_t Rpad = (p.R + 255) / 256 * 256;
     const int tile_rows = OP == OP_GLU ? 256 : p.tile_rows;
+    // rows per band of the tile order: OP_GLU's rows have two weights each (8192
+    // tokens, 11008 x 4096: 492 MB read with 2816 rows and streamed outputs, 631
+    // with 4096 and plain stores, 681 us against 692 at the power cap)
+    constexpr int band_rows = OP == OP_GLU ? 2816 : static_cast<int>(BAND_ROWS);
     const int64_t n_t = (T + bn - 1) / bn;
     const int64_t n_m = (Rpad + tile_rows - 1) / tile_rows;
     const int64_t ntiles = n_t * n_m;
@@ -209,7 +214,7 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
         bool ok = true, dep_done = p.early == 0;
         for (int64_t tile = cluster; tile < ntiles && ok; tile += nclusters) {
             int64_t nt, mt;
-            tile_coords(tile, n_t, n_m, BAND_ROWS / tile_rows, nt, mt);
+            tile_coords(tile, n_t, n_m, band_rows / tile_rows, nt, mt);
             const bool has1 = second(mt);
             const int32_t arow = static_cast<int32_t>(mt * tile_rows + rank * 128);
             const int32_t arow1 = OP == OP_GLU ? arow : arow + 256;
@@ -302,7 +307,7 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
             bool ok = true, dep_done = p.early == 0;
             for (int64_t tile = cluster; tile < ntiles && ok; tile += nclusters, ++ti) {
                 int64_t nt, mt;
-                tile_coords(tile, n_t, n_m, BAND_ROWS / tile_rows, nt, mt);
+                tile_coords(tile, n_t, n_m, band_rows / tile_rows, nt, mt);
                 const bool has1 = second(mt);
                 if (ti >= 1 && !mbar_wait_cluster(acc_empty, static_cast<uint32_t>((ti - 1) & 1))) break;
                 tc_fence_after();
@@ -373,7 +378,7 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
         int64_t ti = 0;
         for (int64_t tile = cluster; tile < ntiles; tile += nclusters, ++ti) {
             int64_t nt, mt;
-            tile_coords(tile, n_t, n_m, BAND_ROWS / tile_rows, nt, mt);
+            tile_coords(tile, n_t, n_m, band_rows / tile_rows, nt, mt);
             if (!__all_sync(0xffffffffu, mbar_wait(acc_full, static_cast<uint32_t>(ti & 1)))) break;
             tc_fence_after();
             const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
@@ -520,7 +525,10 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
                         if (c * 16 + tok < nv && r < p.R) {
                             uint16_t *o = dst + (tok0 + c * 16 + tok) * ld + r;
                             if (r + 8 <= p.R) {
-                                *reinterpret_cast<uint4 *>(o) = v;
+                                if (p.stream_out)
+                                    __stcs(reinterpret_cast<uint4 *>(o), v);
+                                else
+                                    *reinterpret_cast<uint4 *>(o) = v;
                             } else {
                                 const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -1234,6 +1242,7 @@ nm_status launch_ffn(const FfnMaps &maps, FfnArgs p, const FfnPlan &plan, cudaSt
     p.stage_bytes = Cfg::stage_bytes(plan.bn);
     p.sum_off = plan.sum_off;
     p.tile_rows = plan.tile_rows;
+    p.stream_out = (p.G ? 3 : 1) * p.T * p.R * 2 > (64ll << 20) ? 1 : 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(2 * plan.split * plan.clusters), 1, 1);
     cfg.blockDim = dim3(ffn_threads(plan.split > 1), 1, 1);

@@ -82,6 +82,7 @@ CASES = {
     "prompts, rank 128, 8:10": (1500, 264, 515, 10, 128, 3, [7, 400, 400, 900, 1301, 1490], [2, 0, -1, 1, 2]),
     "prompts, rank 8": (2000, 300, 40, 4, 8, 2, [0, 1000, 1010, 2000], [1, 0, 1]),
     "prompts, rank 72, 6:8": (1030, 520, 1030, 8, 72, 5, [0, 100, 330, 331, 1030], [4, 2, 0, 4]),
+    "streamed outputs": (3100, 11001, 64, 4, 16, 3, [0, 1200, 3099], [2, 0]),
     "many short requests over tiles": (600, 256, 128, 8, 8, 200, list(range(0, 601, 3)), [(3 * i) % 200 for i in range(200)]),
 }
 
