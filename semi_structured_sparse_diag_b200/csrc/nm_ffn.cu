@@ -21,10 +21,10 @@
 // Where the time goes (device time, 11008 x 4096 2:4 projections): one token
 // through gate and up 20.0 us, 101 MB of operands at 5.1 TB/s (78% of a measured
 // copy): HBM, and some 5 us of start and tail.  8192 tokens with G and U kept
-// 720 us in a long run, which the power cap bounds (1.4 GHz); 494 us at
-// 1965 MHz, the tensor pipe 69% active: 15 us of products and 5 us of epilogue a
+// 713 us in a long run, which the power cap bounds (1.4 GHz); 494 us at
+// 1965 MHz, the tensor pipe 68% active: 15 us of products and 5 us of epilogue a
 // tile, the latter bound by all SMs' stores at once.  8192 tokens with rank 64
-// adapters 370 us, of which the product 296 and V 41.
+// adapters 355 to 380 us, of which the product 284 and V 41.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -494,11 +494,11 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
                 // the layout of a matrix fragment, transposed by stmatrix on the way to
                 // the warp's 1 KB of shared memory ([token][32 rows], 16-byte pieces
                 // swizzled against bank conflicts), and out as 64 bytes a token.  (Two-byte
-                // stores straight from registers, a row to each lane, took 14 us a tile where
-                // the products take 15 and this takes 5: 820 us against 720 for 8192
-                // tokens of the 7B-shaped projections with G and U kept, 494 against 524
-                // with eight warps at 1965 MHz.)  The accumulators are released once the
-                // last chunk is in registers.
+                // stores straight from registers, a row to each lane, took 14 us a tile
+                // where the products take 15 and this takes 5, for 8192 tokens through
+                // 11008 x 4096 projections with G and U kept; with eight warps instead of
+                // sixteen the kernel took 524 us instead of 494 at 1965 MHz.)  The
+                // accumulators are released once the last chunk is in registers.
                 const int64_t row0 = mt * tile_rows + acc0 * 256 + rank * 128 + q * 32;
                 const uint32_t buf = smem_u32(smem) + C::OFF_OUT + static_cast<uint32_t>(warp - 4) * 1024u;
                 const int bi = lane >> 3, st_tok = (lane & 7) + 8 * (bi >> 1);
