@@ -450,6 +450,11 @@ nm_status nm_sparse_densify(const uint16_t *vals, const uint32_t *mask, int64_t 
  *       All strides multiples of 8.  r a multiple of 8, 8 <= r <=
  *       NM_LORA_MAX_RANK (else NM_ERR_UNSUPPORTED); adapters of lower rank are
  *       padded with zero rows of A.   scale : [adapters] fp32.
+ *       B must be finite: a tile of up to 240 tokens multiplies the B of every
+ *       adapter among them by all of its tokens, with V = 0 for the tokens of
+ *       other adapters, so an infinity or NaN in B[a] makes NaN of the same
+ *       output features of those too.  Those of X, A and scale stay with their
+ *       token or adapter.
  *   indptr : int32 [requests + 1], ids : int32 [requests], on the device.
  *       Request i has the tokens [indptr[i], indptr[i+1]), possibly none, and
  *       adapter ids[i], or none where ids[i] is -1.  Requests may share

@@ -639,7 +639,8 @@ def sparse_gemm_lora(X, packed, R, m, A, B, scale, indptr, ids, Y=None, ws=None,
     """Y = X * W_sparse^T plus, for the tokens indptr[i] .. indptr[i+1] of request
     i, scale[a] (X A[a]^T) B[a]^T with a = ids[i] (-1: no adapter).  A
     [adapters x r x K], B [adapters x R x r] bf16, scale fp32 [adapters],
-    indptr int32 [requests + 1], ids int32 [requests], all on the device."""
+    indptr int32 [requests + 1], ids int32 [requests], all on the device.  B must
+    be finite (a tile's tokens share the product with every adapter among them)."""
     T, K = _two_d(X, "X")
     _bf16(A, "A")
     if A.dim() != 3:

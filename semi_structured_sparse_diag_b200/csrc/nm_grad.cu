@@ -40,7 +40,9 @@ __device__ __forceinline__ void act_and_slope(float g, int act, float &f, float 
     const float z2 = 1.5957691216057308f * (g + 0.044715f * g * g * g);
     const float s = __fdividef(1.0f, 1.0f + __expf(-z2));
     f = g * s;
-    d = s + g * s * (1.0f - s) * 1.5957691216057308f * (1.0f + 0.134145f * g * g);
+    // where s (1 - s) has vanished the slope is s, though g^2 may overflow
+    const float t = s * (1.0f - s);
+    d = t == 0.0f ? s : s + g * t * 1.5957691216057308f * (1.0f + 0.134145f * g * g);
 }
 
 // dG and dU, one rounding to bf16 each (they are tensor-core operands next).

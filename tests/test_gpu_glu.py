@@ -288,3 +288,51 @@ def test_densify_reports_a_wrong_mask(nm):
     nm.sparse_densify(vals, mask, 8, 64, 2, 4)
     with pytest.raises(nm.NMError, match="NM_ERR_DEVICE"):
         nm.check_device_error()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "relu2"])
+def test_backward_at_large_gates(nm, act):
+    # gates where the sigmoid has reached 0 or 1 and g^2 leaves fp32: the slope is
+    # the asymptote's (2 g for relu^2, whose gate stays below 1e18 here)
+    T, R, K = 8, 64, 64
+    big = 1e18 if act == "relu2" else 3e38
+    G = torch.tensor([0.0, 1e4, -1e4, 1e9, -1e9, 1e12, big, -big]).to(torch.bfloat16).cuda()[:, None].expand(T, R).contiguous()
+    U, dH = randn(T, R, 1.0, seed=1), randn(T, R, 1e-20, seed=2)
+    W = torch.eye(R, K, dtype=torch.bfloat16, device="cuda")
+    dX, _, _ = nm.sparse_glu_backward(dH, randn(T, K, 1.0, seed=3), G, U, W, torch.zeros_like(W), act=act)
+    _sync_ok(nm)
+    g = G.double()
+    slope = 2 * g.clamp(min=0) if act == "relu2" else torch.where(g == 0, 0.5, (g > 0).double())
+    want = dH.double() * U.double() * slope  # W is the identity: dX = dG
+    assert_within(dX, want, (2 * HALF_STEP + 2.0 ** -15) * want.abs() + 1e-38, "dX")
+
+
+def test_first_call_captured():
+    # nothing has to run before a capture: in a process of its own
+    import subprocess
+    import sys
+    code = """
+import sys
+sys.path[:0] = ["tests", "."]
+import torch
+import semi_structured_sparse_diag_b200 as nm
+from ffn_testutil import layer, randn
+X, dH = randn(40, 256, 1.0, 1), randn(40, 300, 1.0, 2)
+side, A, B = layer(nm, 300, 256, 8, 3), randn(16, 256, 1.0, 4).view(2, 8, 256), randn(600, 8, 1.0, 5).view(2, 300, 8)
+scale, indptr, ids = torch.ones(2, device="cuda"), torch.tensor([0, 20, 40], dtype=torch.int32, device="cuda"), torch.tensor([1, 0], dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+def step():
+    H, G, U = nm.sparse_glu(X, side["packed"], side["packed"], 300, 8, save=True)
+    return (H, G, U, nm.sparse_gemm_lora(X, side["packed"], 300, 8, A, B, scale, indptr, ids),
+            *nm.sparse_glu_backward(dH, X, G, U, side["dense"], side["dense"]))
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    outs = step()
+g.replay()
+torch.cuda.synchronize()
+nm.check_device_error()
+assert all(torch.equal(a, b) for a, b in zip(outs, step()))
+print("same")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
