@@ -1192,35 +1192,54 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------------------
-// a5 (standalone): activation lift.  One thread per (token, group); window w
-// of a group is the column pairs (w, w+1) of that group, as 32-bit words.
+// a5 (standalone): activation lift.  Window w of a group is the column pairs
+// (w, w+1) of that group, as 32-bit words.
+// A thread takes a group of LIFT_TOKENS consecutive tokens, every load before the
+// first store; two windows leave in a 16-byte store where their count is even.
+// grid: x over groups, y (+65535 z) over token runs.
 // ---------------------------------------------------------------------------
+constexpr int LIFT_TOKENS = 4;
+
+template <int M>
 __global__ void __launch_bounds__(256)
-    k_lift(const uint16_t *__restrict__ X, int64_t T, int64_t K, int64_t ldx, int m, int64_t G,
+    k_lift(const uint16_t *__restrict__ X, int64_t T, int64_t K, int64_t ldx, int64_t G,
            uint16_t *__restrict__ XL, int64_t ldxl) {
     grid_dep_wait();
     grid_dep_launch();
-    const int Ns = m / 2, nwin = Ns - 1;
+    constexpr int NS = M / 2, NWIN = NS - 1;
     const int64_t g = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-    const int64_t t = blockIdx.y;
-    if (g >= G || t >= T) return;
-    const uint16_t *src = X + t * ldx + g * m;
-    uint16_t *dst = XL + t * ldxl + g * nwin * 4;
-    uint32_t x[8];  // m/2 column pairs
-    if (g * m + m <= K) {
-        for (int p = 0; p < Ns; ++p) x[p] = __ldg(reinterpret_cast<const uint32_t *>(src) + p);
-    } else {
-        for (int p = 0; p < Ns; ++p) {
-            const int64_t c = g * m + 2 * p;
-            const uint32_t a = c < K ? __ldg(src + 2 * p) : 0u;
-            const uint32_t b = c + 1 < K ? __ldg(src + 2 * p + 1) : 0u;
-            x[p] = a | (b << 16);
+    const int64_t t0 = (blockIdx.y + static_cast<int64_t>(blockIdx.z) * 65535) * LIFT_TOKENS;
+    if (g >= G || t0 >= T) return;
+    uint32_t x[LIFT_TOKENS][NS];  // column pairs
+#pragma unroll
+    for (int u = 0; u < LIFT_TOKENS; ++u) {
+        const int64_t t = t0 + u < T ? t0 + u : t0;
+        const uint16_t *src = X + t * ldx + g * M;
+        if (g * M + M <= K) {
+#pragma unroll
+            for (int p = 0; p < NS; ++p) x[u][p] = __ldg(reinterpret_cast<const uint32_t *>(src) + p);
+        } else {
+#pragma unroll
+            for (int p = 0; p < NS; ++p) {
+                const int64_t c = g * M + 2 * p;
+                const uint32_t a = c < K ? __ldg(src + 2 * p) : 0u;
+                const uint32_t b = c + 1 < K ? __ldg(src + 2 * p + 1) : 0u;
+                x[u][p] = a | (b << 16);
+            }
         }
     }
-    uint32_t *d32 = reinterpret_cast<uint32_t *>(dst);
-    for (int w = 0; w < nwin; ++w) {
-        d32[2 * w] = x[w];
-        d32[2 * w + 1] = x[w + 1];
+#pragma unroll
+    for (int u = 0; u < LIFT_TOKENS; ++u) {
+        if (t0 + u >= T) break;
+        uint16_t *dst = XL + (t0 + u) * ldxl + g * NWIN * 4;
+        if (NWIN % 2 == 0) {
+#pragma unroll
+            for (int w = 0; w < NWIN; w += 2)
+                reinterpret_cast<uint4 *>(dst)[w / 2] = make_uint4(x[u][w], x[u][w + 1], x[u][w + 1], x[u][w + 2 < NS ? w + 2 : 0]);
+        } else {
+#pragma unroll
+            for (int w = 0; w < NWIN; ++w) reinterpret_cast<uint2 *>(dst)[w] = make_uint2(x[u][w], x[u][w + 1]);
+        }
     }
 }
 
@@ -1801,9 +1820,16 @@ extern "C" nm_status lift_activations(const uint16_t *X, int64_t T, int64_t K, i
     const int64_t KL = G * (m / 2 - 1) * 4;
     if (T < 1 || K < 1 || ldx < K || ldxl < KL) return NM_ERR_SHAPE;
     if (!aligned16(X) || !aligned16(XL) || (ldx % 8) != 0 || (ldxl % 8) != 0) return NM_ERR_ALIGN;
-    if (T > 65535) return NM_ERR_SHAPE;
-    dim3 grid(static_cast<unsigned>((G + 255) / 256), static_cast<unsigned>(T));
-    return launch_dependent(k_lift, grid, 256, as_stream(stream), X, T, K, ldx, m, G, XL, ldxl) ? NM_OK : NM_ERR_CUDA;
+    const int64_t runs = (T + LIFT_TOKENS - 1) / LIFT_TOKENS;
+    if (runs > 65535LL * 65535LL) return NM_ERR_SHAPE;
+    const dim3 grid(static_cast<unsigned>((G + 255) / 256), static_cast<unsigned>(runs < 65535 ? runs : 65535),
+                    static_cast<unsigned>((runs + 65534) / 65535));
+    const cudaStream_t s = as_stream(stream);
+    const bool ok = m == 4   ? launch_dependent(k_lift<4>, grid, 256, s, X, T, K, ldx, G, XL, ldxl)
+                    : m == 6 ? launch_dependent(k_lift<6>, grid, 256, s, X, T, K, ldx, G, XL, ldxl)
+                    : m == 8 ? launch_dependent(k_lift<8>, grid, 256, s, X, T, K, ldx, G, XL, ldxl)
+                             : launch_dependent(k_lift<10>, grid, 256, s, X, T, K, ldx, G, XL, ldxl);
+    return ok ? NM_OK : NM_ERR_CUDA;
 }
 
 extern "C" size_t nm_ternary_workspace_bytes(int64_t R) {
