@@ -1503,11 +1503,17 @@ extern "C" nm_status nm_sparse_gemm_lora(const uint16_t *X, int64_t T, int64_t K
         a.tile_base = tile_base;
         a.slot_adapter = slot_adapter;
         a.V = V;
-        // prompts: at least 16 tokens a request on average, and enough of them that
-        // the wide kernel's start (some 8 us) is less than what the L1 cache costs
-        // the other (8192 tokens, rank 64: 41 us against 92; 777, rank 8: 15.8
-        // against 12.5)
-        if (T >= 16 * requests && T >= 1024) {
+        // Prompts take the wide kernel.  Its cost goes with the slots of a tile, the
+        // other's with the tokens times the columns, so it needs enough tokens in all
+        // (its start is some 8 us: 777 tokens, rank 8: 15.8 us against 12.5), columns
+        // (8192 tokens of 16 requests, rank 16, whole call: 712 columns 35.8 us
+        // against 25.2, 1000 columns 36.4 against 52.2) and tokens a request; the more
+        // of these, the smaller the rank (1500 columns, rank 64, 64 tokens a request:
+        // 65.8 against 87.6, 17: 119.8 against 99.9; rank 16: 57.7 against 57.4 at 64,
+        // 96.3 against 63.2 at 17; 4096 columns, rank 16: 154 against 185 at 64, 217
+        // against 174 at 17; all of 8192 tokens).
+        if (T >= 1024 && K >= 896 && T >= 16 * requests &&
+            (r > 16 || (T >= 32 * requests && T * K >= 131072 * requests))) {
             CUtensorMap tx, ta;
             if (!set_smem_attr<k_lora_shrink_wide>(WideShrink::SMEM_BYTES) ||
                 !make_tmap_bf16(&tx, X, T, K, ldx, 64, 128, true) ||

@@ -336,3 +336,19 @@ print("same")
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=240)
     assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("T,m", [(65539, 6), (65536, 10), (262147, 6)])
+def test_glu_of_many_tokens(nm, T, m):
+    # past 65535 tokens, and past as many runs of the staging kernel's four
+    R, K = 24, 22
+    X = randn(T, K, 1.0, seed=T)
+    gate, up = layer(nm, R, K, m, seed=1), layer(nm, R, K, m, seed=2)
+    out = nm.sparse_glu(X, gate["packed"], up["packed"], R, m, act="silu")
+    lifted = nm.lift_activations(X, m)
+    _sync_ok(nm)
+    _check_glu(X, gate, up, "silu", out)
+    g = (K + m - 1) // m
+    pairs = torch.nn.functional.pad(X, (0, g * m - K)).reshape(T, g, m // 2, 2)
+    want = torch.stack((pairs[:, :, :-1], pairs[:, :, 1:]), 3).reshape(T, -1)
+    assert torch.equal(lifted[:, :want.shape[1]], want)

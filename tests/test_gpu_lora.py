@@ -83,6 +83,12 @@ CASES = {
     "prompts, rank 8": (2000, 300, 40, 4, 8, 2, [0, 1000, 1010, 2000], [1, 0, 1]),
     "prompts, rank 72, 6:8": (1030, 520, 1030, 8, 72, 5, [0, 100, 330, 331, 1030], [4, 2, 0, 4]),
     "streamed outputs": (3100, 11001, 64, 4, 16, 3, [0, 1200, 3099], [2, 0]),
+    "long prompts, rank 128, 8:10": (1500, 264, 1003, 10, 128, 3, [7, 400, 400, 900, 1301, 1490], [2, 0, -1, 1, 2]),
+    "long prompts, rank 8": (2000, 300, 1100, 4, 8, 2, [0, 1000, 1010, 2000], [1, 0, 1]),
+    "streamed outputs of prompts": (3100, 11001, 904, 4, 16, 3, [0, 1200, 3099], [2, 0]),
+    "prompts of five tokens and of a thousand": (1200, 260, 960, 4, 72, 9, [0, *range(100, 201, 5), 1200],
+                                                 [i % 10 - 1 for i in range(22)]),
+    "prompts of 24 tokens, rank 16": (1440, 300, 1003, 6, 16, 6, list(range(0, 1441, 24)), [(5 * i) % 7 - 1 for i in range(60)]),
     "many short requests over tiles": (600, 256, 128, 8, 8, 200, list(range(0, 601, 3)), [(3 * i) % 200 for i in range(200)]),
 }
 
