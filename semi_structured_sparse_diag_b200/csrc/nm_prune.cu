@@ -1196,6 +1196,9 @@ __global__ void __launch_bounds__(256)
 // (w, w+1) of that group, as 32-bit words.
 // A thread takes a group of LIFT_TOKENS consecutive tokens, every load before the
 // first store; two windows leave in a 16-byte store where their count is even.
+// Bound by the rate of its memory instructions: one token a thread with 4-byte
+// stores cost a gated feed-forward of 5397 tokens, 328 x 2231, 8:10 49.1 us in
+// all, this 36.1 us (1 token each or 4 is within 2% at 64 tokens).
 // grid: x over groups, y (+65535 z) over token runs.
 // ---------------------------------------------------------------------------
 constexpr int LIFT_TOKENS = 4;
