@@ -431,6 +431,18 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
     }
 }
 
+// The same waits for a warp that stays in step: every lane waits, and all of them
+// get the same answer.  A wait's limit is each lane's own clock, so near it some
+// lanes may see the barrier and others give up; a loop that went on or ended lane
+// by lane would leave half of a warp at the next warp-wide instruction for good.
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
+__device__ __forceinline__ bool mbar_wait_cluster_warp(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity));
+}
+
 // TMA tile load of a CTA pair: data lands in this CTA's shared memory, the
 // completed byte count is signalled on `bar_cluster` (the leader CTA's barrier).
 __device__ __forceinline__ void tma_load_2d_pair(void *smem_dst, const void *tmap,

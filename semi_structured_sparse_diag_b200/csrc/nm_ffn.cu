@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
                     grid_dep_wait();
                     dep_done = true;
                 }
-                if (it >= S && !mbar_wait(&empty[s], ph ^ 1u)) { ok = false; break; }
+                if (it >= S && !mbar_wait_warp(&empty[s], ph ^ 1u)) { ok = false; break; }
                 if (lead) {
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], tx);
                     const uint32_t bar = full0 + static_cast<uint32_t>(s) * 8u;
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
                 const int per = 64 / p.width, piece = p.width * 2;  // bytes per row of a piece
                 int32_t a_next = x0 < x1 ? __ldcg(p.slot_adapter + slot0 + x0 / p.rb) : 0;
                 for (int x = x0; x < x1; x += per, ++it) {
-                    if (it >= S && !mbar_wait(&empty[s], ph ^ 1u)) { ok = false; break; }
+                    if (it >= S && !mbar_wait_warp(&empty[s], ph ^ 1u)) { ok = false; break; }
                     const int n = x1 - x < per ? x1 - x : per;
                     const uint32_t bar = full0 + static_cast<uint32_t>(s) * 8u;
                     const uint32_t st = st0 + static_cast<uint32_t>(s) * p.stage_bytes;
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
         }
         if (!ok && rank == 0) {  // let copies already issued land before exiting
             for (int64_t j = (it > S ? it - S : 0); j < it; ++j)
-                mbar_wait(&full[j % S], static_cast<uint32_t>((j / S) & 1));
+                mbar_wait_warp(&full[j % S], static_cast<uint32_t>((j / S) & 1));
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA issuer
@@ -309,10 +309,10 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
                 int64_t nt, mt;
                 tile_coords(tile, n_t, n_m, band_rows / tile_rows, nt, mt);
                 const bool has1 = second(mt);
-                if (ti >= 1 && !mbar_wait_cluster(acc_empty, static_cast<uint32_t>((ti - 1) & 1))) break;
+                if (ti >= 1 && !mbar_wait_cluster_warp(acc_empty, static_cast<uint32_t>((ti - 1) & 1))) break;
                 tc_fence_after();
                 for (int kb = 0; kb < nblocks; ++kb) {
-                    if (!mbar_wait(&full[s], ph)) { ok = false; break; }
+                    if (!mbar_wait_warp(&full[s], ph)) { ok = false; break; }
                     tc_fence_after();
                     const uint64_t so = static_cast<uint64_t>(static_cast<uint32_t>(s) * step);
                     if (lead) {
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
                     const int per = 64 / p.width, piece = p.width * 2, steps = p.width / 16;
                     const uint32_t layout = p.width == 16 ? 6 : (p.width == 32 ? 4 : 2);
                     for (int x = x0; x < x1; x += per) {  // on top of this pair's K' blocks
-                        if (!mbar_wait(&full[s], ph)) { ok = false; break; }
+                        if (!mbar_wait_warp(&full[s], ph)) { ok = false; break; }
                         tc_fence_after();
                         if (lead) {
                             const uint32_t st = st0 + static_cast<uint32_t>(s) * p.stage_bytes;
@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
         for (int64_t tile = cluster; tile < ntiles; tile += nclusters, ++ti) {
             int64_t nt, mt;
             tile_coords(tile, n_t, n_m, band_rows / tile_rows, nt, mt);
-            if (!__all_sync(0xffffffffu, mbar_wait(acc_full, static_cast<uint32_t>(ti & 1)))) break;
+            if (!mbar_wait_warp(acc_full, static_cast<uint32_t>(ti & 1))) break;
             tc_fence_after();
             const uint32_t tq = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
             const int acc0 = by_tokens ? 0 : grp & 1;  // the (first) accumulator of this warp
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
             if constexpr (SPLIT) {
                 // this CTA's sums in its shared memory: [accumulator][4 tokens][row][token], fp32
                 float4 *mine = reinterpret_cast<float4 *>(smem + p.sum_off) + acc0 * (bn / 4) * 128 + q * 32 + lane;
-                if (ti >= 1 && !__all_sync(0xffffffffu, mbar_wait_cluster(sum_free, static_cast<uint32_t>((ti - 1) & 1))))
+                if (ti >= 1 && !mbar_wait_cluster_warp(sum_free, static_cast<uint32_t>((ti - 1) & 1)))
                     break;
 #pragma unroll 1
                 for (int c = c_lo; c < c_hi; ++c) {
@@ -424,7 +424,7 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(acc_empty_cl);
                 if (lane < split) mbar_arrive_cluster(mapa_shared(sum_ready, 2 * lane + rank));
-                if (!__all_sync(0xffffffffu, mbar_wait_cluster(sum_ready, static_cast<uint32_t>(ti & 1)))) break;
+                if (!mbar_wait_cluster_warp(sum_ready, static_cast<uint32_t>(ti & 1))) break;
                 // this pair's share of the tokens, four at a time; all the parts of
                 // GROUPS x 4 tokens are in flight before the first is used
                 constexpr int GROUPS = OP == OP_GLU ? 1 : 2;
@@ -997,7 +997,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 2)
             int ls = s, li = it;
             uint32_t lp = ph;
             for (int kb = kb0; kb < kb1 && ok; ++kb, ++li) {
-                if (li >= C::STAGES && !mbar_wait(&empty[ls], lp ^ 1u)) ok = false;
+                if (li >= C::STAGES && !mbar_wait_warp(&empty[ls], lp ^ 1u)) ok = false;
                 if (ok && lead) {
                     uint8_t *st = smem + ls * C::STAGE_BYTES;
                     mbar_arrive_expect_tx(&full[ls], static_cast<uint32_t>((two ? C::X_BYTES : C::X_BYTES / 2) + C::A_BYTES));
@@ -1016,7 +1016,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 2)
             int ls = s;
             uint32_t lp = ph;
             for (int kb = kb0; kb < kb1 && ok; ++kb) {
-                if (!mbar_wait(&full[ls], lp)) ok = false;
+                if (!mbar_wait_warp(&full[ls], lp)) ok = false;
                 tc_fence_after();
                 if (ok && lead) {
                     const uint64_t so = static_cast<uint64_t>(static_cast<uint32_t>(ls) * (C::STAGE_BYTES >> 4));
@@ -1039,7 +1039,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 2)
         if (s >= C::STAGES) s -= C::STAGES;
         ph = static_cast<uint32_t>((it / C::STAGES) & 1);
         if (n > 0) {
-            if (!mbar_wait(done, dph)) ok = false;
+            if (!mbar_wait_warp(done, dph)) ok = false;
             dph ^= 1u;
         }
         tc_fence_after();
@@ -1094,7 +1094,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 2)
     // a wait that ran out: let copies already issued land before exiting
     if (!ok && warp == 0)
         for (int q = it > C::STAGES ? it - C::STAGES : 0; q < it; ++q)
-            mbar_wait(&full[q % C::STAGES], static_cast<uint32_t>((q / C::STAGES) & 1));
+            mbar_wait_warp(&full[q % C::STAGES], static_cast<uint32_t>((q / C::STAGES) & 1));
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {

@@ -261,13 +261,13 @@ __global__ void __launch_bounds__(GradCfg::THREADS, 1)
             const int32_t n0 = static_cast<int32_t>(nt * 256 + rank * 128);
             // SPLIT: the sums of the tile of dX lie over the stages until all have read them
             if (SPLIT && shared_sums) {
-                if (!mbar_wait_cluster(sum_free, 0)) { ok = false; break; }
+                if (!mbar_wait_cluster_warp(sum_free, 0)) { ok = false; break; }
                 fence_proxy_async_smem();
             }
             shared_sums = SPLIT && is_x;
             const int v1 = is_x ? x1 : nkt;
             for (int v = is_x ? x0 : 0; v < v1; ++v, ++it) {
-                if (it >= S && !mbar_wait(&empty[s], ph ^ 1u)) { ok = false; break; }
+                if (it >= S && !mbar_wait_warp(&empty[s], ph ^ 1u)) { ok = false; break; }
                 if (lead) {
                     if (rank == 0) mbar_arrive_expect_tx(&full[s], 2u * C::STAGE_BYTES);
                     const uint32_t bar = full0 + static_cast<uint32_t>(s) * 8u;
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(GradCfg::THREADS, 1)
         }
         if (!ok && rank == 0) {  // let copies already issued land before exiting
             for (int64_t j = (it > S ? it - S : 0); j < it; ++j)
-                mbar_wait(&full[j % S], static_cast<uint32_t>((j / S) & 1));
+                mbar_wait_warp(&full[j % S], static_cast<uint32_t>((j / S) & 1));
         }
     } else if (warp == 1) {
         // ---------------------------------------------------------- MMA issuer
@@ -312,14 +312,14 @@ __global__ void __launch_bounds__(GradCfg::THREADS, 1)
             for (; ok && tiles.next(is_x, src, tile); ++ti) {
                 const int buf = static_cast<int>(ti & 1);
                 const uint32_t aph = static_cast<uint32_t>((ti >> 1) & 1);
-                if (ti >= 2 && !mbar_wait_cluster(&acc_empty[buf], aph ^ 1u)) break;
+                if (ti >= 2 && !mbar_wait_cluster_warp(&acc_empty[buf], aph ^ 1u)) break;
                 tc_fence_after();
                 const uint32_t dcol = tmem_base + static_cast<uint32_t>(buf * 256);
                 const int n = is_x ? x1 - x0 : nkt;
                 const uint64_t ad = is_x ? ak : am, astep = is_x ? 32 >> 4 : 2048 >> 4;
                 const uint32_t id = idesc | (is_x ? 0u : 1u << 15);
                 for (int v = 0; v < n; ++v) {
-                    if (!mbar_wait(&full[s], ph)) { ok = false; break; }
+                    if (!mbar_wait_warp(&full[s], ph)) { ok = false; break; }
                     tc_fence_after();
                     const uint64_t so = static_cast<uint64_t>(static_cast<uint32_t>(s) * (C::STAGE_BYTES >> 4));
                     if (lead) {
@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(GradCfg::THREADS, 1)
             int64_t nt, mt;
             tile_coords(tile, n_n, is_x ? m_x : m_w, BAND, nt, mt);
             const int buf = static_cast<int>(ti & 1);
-            if (!__all_sync(0xffffffffu, mbar_wait(&acc_full[buf], static_cast<uint32_t>((ti >> 1) & 1)))) break;
+            if (!mbar_wait_warp(&acc_full[buf], static_cast<uint32_t>((ti >> 1) & 1))) break;
             tc_fence_after();
             const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                 static_cast<uint32_t>(buf * 256 + h * 128);
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(GradCfg::THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(buf ? acc_empty1 : acc_empty0);
                     if (lane < split) mbar_arrive_cluster(mapa_shared(sum_ready, 2 * lane + rank));
-                    if (!__all_sync(0xffffffffu, mbar_wait_cluster(sum_ready, 0))) break;
+                    if (!mbar_wait_cluster_warp(sum_ready, 0)) break;
                     const uint32_t off = smem_u32(mine);
                     uint32_t from[C::MAX_SPLIT];
 #pragma unroll
