@@ -994,11 +994,8 @@ __global__ void __launch_bounds__(PairCfg<MODE>::THREADS, 1)
                 // nothing; after one wait times out the rest are not waited for
                 bool got = true;
                 for (int64_t cc = cluster + 1; cc <= last_contrib && got; ++cc)
-                    if ((cc + 1) * total / nclusters > cc * total / nclusters) {
-                        uint64_t *fl = flags + (cc * 2 + rank) * 8 + we;
-                        got = sk_wait_flag(fl, seq);
-                        sk_clear_flag(fl, lane, got);
-                    }
+                    if ((cc + 1) * total / nclusters > cc * total / nclusters)
+                        got = sk_take_flag(flags + (cc * 2 + rank) * 8 + we, seq, lane);
             }
             uint32_t packed[64];
 #pragma unroll

@@ -130,7 +130,7 @@ __device__ __forceinline__ uint64_t ld_acquire_u64(const uint64_t *p) {
     return v;
 }
 
-// bounded wait for a stream-K flag (all lanes poll; one second limit)
+// bounded wait for a stream-K flag (one lane's answer; one second limit)
 __device__ __forceinline__ bool sk_wait_flag(const uint64_t *p, uint64_t seq) {
     if (ld_acquire_u64(p) == seq) return true;
     const uint64_t t0 = global_timer_ns(), limit = wait_limit_ns();
@@ -144,12 +144,14 @@ __device__ __forceinline__ bool sk_wait_flag(const uint64_t *p, uint64_t seq) {
     }
 }
 
-// A flag has one reader, which clears it once seen: the replay of a captured
-// launch carries the same sequence number, and must not take the partial sums
-// of the replay before it for its own.  (Every lane has polled the flag.)
-__device__ __forceinline__ void sk_clear_flag(uint64_t *p, int lane, bool seen) {
-    __syncwarp();
+// The whole warp's wait for one flag: every lane polls and all get the same
+// answer.  A flag has one reader, which clears it once seen: the replay of a
+// captured launch carries the same sequence number, and must not take the partial
+// sums of the replay before it for its own.
+__device__ __forceinline__ bool sk_take_flag(uint64_t *p, uint64_t seq, int lane) {
+    const bool seen = __all_sync(0xffffffffu, sk_wait_flag(p, seq));
     if (lane == 0 && seen) *static_cast<volatile uint64_t *>(p) = 0;
+    return seen;
 }
 
 // ---------------------------------------------------------------------------

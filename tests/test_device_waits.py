@@ -30,3 +30,13 @@ def test_a_common_wait_is_a_vote():
     for name in ("mbar_wait", "mbar_wait_cluster"):
         body = re.search(rf"bool {name}_warp\([^)]*\) {{(.*?)}}", text, re.S).group(1)
         assert re.fullmatch(rf"\s*return __all_sync\(0xffffffffu, {name}\(bar, parity\)\);\s*", body)
+
+
+def test_stream_k_flags_are_taken_by_the_warp():
+    # a flag is cleared, and the loop over the later flags ended, on one answer of
+    # the warp; the lanes that poll a flag each (k_gemm_wide) vote on all of theirs
+    text = source("nm_gemm.cu")
+    assert re.findall(r"\bgot = ([^;]*);", text).count("sk_take_flag(flags + (cc * 2 + rank) * 8 + we, seq, lane)") == 1
+    assert re.findall(r"(\w+) = sk_wait_flag\(", text) == ["mine"] and "got = __all_sync(0xffffffffu, mine);" in text
+    take = re.search(r"bool sk_take_flag\([^)]*\) {(.*?)\n}", source("nm_gemm.cuh"), re.S).group(1)
+    assert "__all_sync(0xffffffffu, sk_wait_flag(p, seq))" in take and "__syncwarp" not in take
