@@ -424,7 +424,9 @@ nm_status nm_sparse_glu(const uint16_t *X, int64_t T, int64_t K, int64_t ldx, co
  * Two launches: dG and dU, then all three products (dX apart when it is
  * large).  Sums run in a fixed order:
  * repeated calls agree bit for bit.  With few tokens dX's contraction is split
- * over the pairs of a cluster, as above.                                     */
+ * over the pairs of a cluster, as above.  nm_gemm_set_schedule: 1 never splits
+ * it, 2 wherever each of its tiles can have a cluster of its own; its cluster
+ * count bounds the clusters.                                                 */
 size_t nm_sparse_glu_backward_workspace_bytes(int64_t T, int64_t R);
 nm_status nm_sparse_glu_backward(const uint16_t *dH, int64_t lddh, const uint16_t *X, int64_t T, int64_t K,
                                  int64_t ldx, const uint16_t *G, const uint16_t *U, int64_t ldgu,
@@ -490,9 +492,10 @@ nm_status nm_sparse_gemm_lora(const uint16_t *X, int64_t T, int64_t K, int64_t l
 /* Process-wide GEMM schedule, for tests and measurements (not thread-safe
  * against GEMM calls being issued concurrently on other host threads).
  *   policy   : 0 automatic (default), 1 whole tiles only, 2 stream-K whenever
- *              the workspace allows it.
- *   clusters : 0 = as many CTA pairs as fit on the device at once, else at
- *              most this many.
+ *              the workspace allows it (the feed-forward operators: tiles
+ *              split over the pairs of a cluster, see there).
+ *   clusters : 0 = as many CTA pairs (clusters, where a cluster shares a
+ *              tile) as fit on the device at once, else at most this many.
  * Returns NM_ERR_SHAPE for a policy outside 0..2 or clusters < 0.          */
 nm_status nm_gemm_set_schedule(int policy, int clusters);
 

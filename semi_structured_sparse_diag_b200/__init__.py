@@ -681,7 +681,8 @@ def sparse_gemm_lora(X, packed, R, m, A, B, scale, indptr, ids, Y=None, ws=None,
 
 def set_gemm_schedule(policy: int = 0, clusters: int = 0) -> None:
     """GEMM schedule for this process: policy 0 automatic, 1 whole tiles only,
-    2 stream-K whenever the workspace allows; clusters 0 = all that fit."""
+    2 stream-K whenever the workspace allows (the feed-forward operators: tiles
+    split over a cluster's pairs); clusters 0 = all that fit."""
     _check(load().nm_gemm_set_schedule(policy, clusters), "nm_gemm_set_schedule")
 
 

@@ -581,15 +581,19 @@ int64_t grad_clusters(int split) {
 nm_status launch_grad(const GradMaps &maps, GradArgs p, cudaStream_t s) {
     using Cfg = GradCfg;
     // pairs per tile of dX: the least of (contraction blocks of a pair) x ~600
-    // clocks + the exchange of 128 KB of sums at some 18 bytes a clock
+    // clocks + the exchange of 128 KB of sums at some 18 bytes a clock; a split
+    // needs a cluster for every tile.  nm_gemm_set_schedule: 1 never splits, 2
+    // always where that holds, and its cluster count bounds the clusters.
+    const int policy = g_sched_policy.load(), bound = g_sched_clusters.load();
+    auto bounded = [&](int64_t n) { return bound > 0 && bound < n ? static_cast<int64_t>(bound) : n; };
     int split = 1;
-    int64_t clusters = grad_clusters<k_gemm_grad<false>>(1);
+    int64_t clusters = bounded(grad_clusters<k_gemm_grad<false>>(1));
     const int64_t blocks = 2 * ((p.R + 63) / 64);
-    int64_t best = blocks * 600;
-    for (int i = 2; i <= Cfg::MAX_SPLIT && p.tiles_x > 0 && i <= blocks; ++i) {
+    int64_t best = policy == 2 ? INT64_MAX : blocks * 600;
+    for (int i = 2; i <= Cfg::MAX_SPLIT && p.tiles_x > 0 && i <= blocks && policy != 1; ++i) {
         const int64_t cost = (blocks + i - 1) / i * 600 + 10000;
         if (cost >= best) continue;
-        const int64_t n = grad_clusters<k_gemm_grad<true>>(i);
+        const int64_t n = bounded(grad_clusters<k_gemm_grad<true>>(i));
         if (n < p.tiles_x) continue;
         best = cost;
         split = i;
