@@ -594,11 +594,12 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
 // leaves every tile room and needs requests + tiles slots in all.
 //
 // k_lora_shrink, one (tile, slot, rank block of <= 64) per cluster of up to
-// SHRINK_PARTS blocks that split K.  Every block first works out its tile's
-// slots (one pass over the list, a hash of the adapters; about a microsecond,
-// less than a kernel of its own would take to start), then, for its slots,
-// lists the slot's tokens and multiplies 32 of them at a time with mma.sync: a
-// slot of up to 32 tokens has its K split over the warps too, a larger one has
+// SHRINK_PARTS blocks that split K (grid: x over parts and tiles, of which there
+// may be more than 65535, y over slots and rank blocks).  Every block first works
+// out its tile's slots (one pass over the list, a hash of the adapters; about a
+// microsecond, less than a kernel of its own would take to start), then, for its
+// slots, lists the slot's tokens and multiplies 32 of them at a time with mma.sync:
+// a slot of up to 32 tokens has its K split over the warps too, a larger one has
 // groups of 32 tokens side by side in the warps.  A thread's 16-byte loads of X
 // and A cover the same eight columns, which the two k-steps of a block of 32
 // columns take in a permuted order (the same one for both operands), so neither
@@ -767,22 +768,22 @@ __global__ void __launch_bounds__(SHRINK_THREADS)
     grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tg = lane & 3;
     const int part = static_cast<int>(cluster_ctarank()), parts = p.parts;
-    const int64_t tile = blockIdx.y, t0 = tile * p.bn;
-    const int rk = static_cast<int>(blockIdx.z % p.rb) * SHRINK_RANKS;
-    const int lanes_z = gridDim.z / p.rb;
+    const int64_t tile = blockIdx.x / static_cast<unsigned>(parts), t0 = tile * p.bn;
+    const int rk = static_cast<int>(blockIdx.y % p.rb) * SHRINK_RANKS;
+    const int lanes_z = gridDim.y / p.rb;
     const int nr = p.r - rk < NR ? p.r - rk : NR, nn = nr / 8;
     const bool bad = plan_tile(p, tile, plan);
     if (bad) raise_error(ERRBIT_DEVICE);
     const int cnt = plan.cnt;
     const int64_t base = plan.base;
-    if (blockIdx.x == 0 && blockIdx.z == 0) {  // what the product reads
+    if (part == 0 && blockIdx.y == 0) {  // what the product reads
         for (int k = threadIdx.x; k < cnt; k += SHRINK_THREADS) p.slot_adapter[base + k] = plan.adapter[k];
         if (threadIdx.x == 0) {
             p.tile_cnt[tile] = cnt;
             p.tile_base[tile] = static_cast<int32_t>(base);
         }
     }
-    for (int j = blockIdx.z / p.rb; j < cnt; j += lanes_z) {  // the same in every block of the cluster
+    for (int j = blockIdx.y / p.rb; j < cnt; j += lanes_z) {  // the same in every block of the cluster
         uint16_t *vslot = p.V + (base + j) * p.bn * static_cast<int64_t>(p.r) + rk;
         // the slot's tokens in ascending order; the other rows are zero
         uint32_t b[2];
@@ -957,9 +958,9 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 2)
     TilePlan &plan = *reinterpret_cast<TilePlan *>(bars + 16);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = static_cast<int>(cluster_ctarank());
-    const int64_t tile = blockIdx.y, t0 = tile * p.bn;
-    const int rk = static_cast<int>(blockIdx.z % p.rb) * SHRINK_RANKS;
-    const int lanes_z = gridDim.z / p.rb;
+    const int64_t tile = blockIdx.x / SHRINK_PARTS, t0 = tile * p.bn;
+    const int rk = static_cast<int>(blockIdx.y % p.rb) * SHRINK_RANKS;
+    const int lanes_z = gridDim.y / p.rb;
     const int nr = p.r - rk < SHRINK_RANKS ? p.r - rk : SHRINK_RANKS;
     const int nkb = static_cast<int>((p.K + 63) / 64);
     const int kb0 = nkb * part / SHRINK_PARTS, kb1 = nkb * (part + 1) / SHRINK_PARTS;
@@ -987,7 +988,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 2)
     const uint32_t tmem_base = *tmem_slot;
     const int cnt = plan.cnt;
     const int64_t base = plan.base;
-    if (blockIdx.x == 0 && blockIdx.z == 0) {  // what the product reads
+    if (part == 0 && blockIdx.y == 0) {  // what the product reads
         for (int k = threadIdx.x; k < cnt; k += SHRINK_THREADS) p.slot_adapter[base + k] = plan.adapter[k];
         if (threadIdx.x == 0) {
             p.tile_cnt[tile] = cnt;
@@ -997,7 +998,7 @@ __global__ void __launch_bounds__(SHRINK_THREADS, 2)
     int s = 0, it = 0;
     uint32_t ph = 0, dph = 0;
     bool ok = true;
-    for (int j = blockIdx.z / p.rb; j < cnt; j += lanes_z) {  // the same in every block of the cluster
+    for (int j = blockIdx.y / p.rb; j < cnt; j += lanes_z) {  // the same in every block of the cluster
         const int32_t ad = plan.adapter[j];
         if (warp == 0) {
             const bool lead = elect_one() != 0u;
@@ -1271,10 +1272,10 @@ nm_status launch_ffn(const FfnMaps &maps, FfnArgs p, const FfnPlan &plan, cudaSt
 }
 
 template <class Kernel, class... Args>
-nm_status launch_shrink(Kernel kernel, dim3 grid, int smem, cudaStream_t s, const Args &...args) {  // grid.x: the cluster
+nm_status launch_shrink(Kernel kernel, int parts, dim3 grid, int smem, cudaStream_t s, const Args &...args) {
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = grid.x;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(parts);
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1468,7 +1469,6 @@ extern "C" nm_status nm_sparse_gemm_lora(const uint16_t *X, int64_t T, int64_t K
     p.tile_cnt = cap > 0 ? tile_cnt : nullptr;
     p.tile_base = tile_base;
     p.slot_adapter = slot_adapter;
-    if (tiles > 65535) return NM_ERR_SHAPE;
     if (!packed_maps(&maps.a0, &maps.e0, packed, g)) return NM_ERR_CUDA;
     maps.a1 = maps.a0;
     maps.e1 = maps.e0;
@@ -1526,9 +1526,8 @@ extern "C" nm_status nm_sparse_gemm_lora(const uint16_t *X, int64_t T, int64_t K
                 !make_tmap_bf16(&tx, X, T, K, ldx, 64, 128, true) ||
                 !make_tmap_bf16_3d(&ta, A, adapters, r, K, lda, sda, 64, SHRINK_RANKS))
                 return NM_ERR_CUDA;
-            const dim3 grid(static_cast<unsigned>(SHRINK_PARTS), static_cast<unsigned>(tiles),
-                            static_cast<unsigned>((cap < 2 ? cap : 2) * p.rb));
-            st = launch_shrink(k_lora_shrink_wide, grid, WideShrink::SMEM_BYTES, s, a, tx, ta);
+            const dim3 grid(static_cast<unsigned>(SHRINK_PARTS * tiles), static_cast<unsigned>((cap < 2 ? cap : 2) * p.rb));
+            st = launch_shrink(k_lora_shrink_wide, SHRINK_PARTS, grid, WideShrink::SMEM_BYTES, s, a, tx, ta);
             if (st != NM_OK) return st;
             return m == 8 ? launch_ffn<PMODE_SP68T, OP_LORA>(maps, p, plan, s)
                           : launch_ffn<PMODE_SP24, OP_LORA>(maps, p, plan, s);
@@ -1540,11 +1539,11 @@ extern "C" nm_status nm_sparse_gemm_lora(const uint16_t *X, int64_t T, int64_t K
         while (a.parts > 2 && lanes * a.parts > at_once) a.parts /= 2;
         if (lanes * a.parts > 2 * at_once) lanes = 2 * at_once / a.parts + 1;
         if (lanes > cap) lanes = cap;
-        const dim3 grid(static_cast<unsigned>(a.parts), static_cast<unsigned>(tiles), static_cast<unsigned>(lanes * p.rb));
-        st = r <= 8    ? launch_shrink(k_lora_shrink<1>, grid, 0, s, a)
-             : r <= 16 ? launch_shrink(k_lora_shrink<2>, grid, 0, s, a)
-             : r <= 32 ? launch_shrink(k_lora_shrink<4>, grid, 0, s, a)
-                       : launch_shrink(k_lora_shrink<8>, grid, 0, s, a);
+        const dim3 grid(static_cast<unsigned>(a.parts * tiles), static_cast<unsigned>(lanes * p.rb));
+        st = r <= 8    ? launch_shrink(k_lora_shrink<1>, a.parts, grid, 0, s, a)
+             : r <= 16 ? launch_shrink(k_lora_shrink<2>, a.parts, grid, 0, s, a)
+             : r <= 32 ? launch_shrink(k_lora_shrink<4>, a.parts, grid, 0, s, a)
+                       : launch_shrink(k_lora_shrink<8>, a.parts, grid, 0, s, a);
         if (st != NM_OK) return st;
     }
     return m == 8 ? launch_ffn<PMODE_SP68T, OP_LORA>(maps, p, plan, s)
