@@ -452,11 +452,14 @@ nm_status nm_sparse_densify(const uint16_t *vals, const uint32_t *mask, int64_t 
  *       All strides multiples of 8.  r a multiple of 8, 8 <= r <=
  *       NM_LORA_MAX_RANK (else NM_ERR_UNSUPPORTED); adapters of lower rank are
  *       padded with zero rows of A.   scale : [adapters] fp32.
- *       B must be finite: a tile of up to 240 tokens multiplies the B of every
- *       adapter among them by all of its tokens, with V = 0 for the tokens of
- *       other adapters, so an infinity or NaN in B[a] makes NaN of the same
- *       output features of those too.  Those of X, A and scale stay with their
- *       token or adapter.
+ *       Infinities and NaN of X, A, B and scale reach the tokens whose
+ *       formula holds them and no others.  A tile multiplies the B of each of
+ *       its adapters by all of its tokens, with V = 0 for those of other
+ *       adapters; outputs that 0 times an infinity or NaN of such a B makes NaN
+ *       are computed again from the token's own adapter, slowly: 64 requests
+ *       of eight adapters, one of them NaN throughout, take 0.9 ms for a 4096 x
+ *       4096 projection in place of 16 us.  (Columns of B that a lower rank
+ *       leaves unused are multiplied by V = 0 as well: keep them finite.)
  *   indptr : int32 [requests + 1], ids : int32 [requests], on the device.
  *       Request i has the tokens [indptr[i], indptr[i+1]), possibly none, and
  *       adapter ids[i], or none where ids[i] is -1.  Requests may share

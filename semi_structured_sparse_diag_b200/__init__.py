@@ -639,8 +639,9 @@ def sparse_gemm_lora(X, packed, R, m, A, B, scale, indptr, ids, Y=None, ws=None,
     """Y = X * W_sparse^T plus, for the tokens indptr[i] .. indptr[i+1] of request
     i, scale[a] (X A[a]^T) B[a]^T with a = ids[i] (-1: no adapter).  A
     [adapters x r x K], B [adapters x R x r] bf16, scale fp32 [adapters],
-    indptr int32 [requests + 1], ids int32 [requests], all on the device.  B must
-    be finite (a tile's tokens share the product with every adapter among them)."""
+    indptr int32 [requests + 1], ids int32 [requests], all on the device.  An
+    infinity or NaN in one adapter reaches that adapter's tokens alone, but slows
+    the call down for all."""
     T, K = _two_d(X, "X")
     _bf16(A, "A")
     if A.dim() != 3:

@@ -85,6 +85,15 @@ struct FfnArgs {
     // no adapters at all
     const int32_t *tile_cnt, *tile_base, *slot_adapter;
     int rb, width;
+    // OP_LORA, for repair_tile: what the tensor maps read, and the requests.  src: the
+    // activations of the K' blocks in order (6:8: of the first two thirds, X; mid:
+    // the rest), src_cols columns
+    const uint16_t *src, *mid, *vals, *B, *V;
+    const uint8_t *meta;
+    int64_t src_ld, src_cols, mid_ld, mid_cols, ldb, sdb;
+    const int32_t *indptr, *ids;
+    int32_t requests;
+    int r;
 };
 
 // silu g / (1 + e^-g); gelu (tanh form) g / (1 + e^-2z), since (1 + tanh z) / 2 =
@@ -108,6 +117,145 @@ __device__ __forceinline__ void gate(float (&g)[N], const float (&u)[N], int act
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i) g[i] = act_fn<ACT_RELU2>(g[i]) * u[i];
+    }
+}
+
+__device__ __forceinline__ float bf16_f32(uint16_t v) { return __uint_as_float(static_cast<uint32_t>(v) << 16); }
+__device__ __forceinline__ bool bf16_nan(uint16_t v) { return (v & 0x7FFFu) > 0x7F80u; }
+
+// columns c .. c + 3 of a row of n columns, zero past its end; c a multiple of 4
+__device__ __forceinline__ uint2 row4(const uint16_t *__restrict__ row, int64_t c, int64_t n) {
+    if (c + 4 <= n) return __ldg(reinterpret_cast<const uint2 *>(row + c));
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        if (c + j < n) w[j >> 1] |= static_cast<uint32_t>(__ldg(row + c + j)) << (16 * (j & 1));
+    return make_uint2(w[0], w[1]);
+}
+
+// A tile multiplies the B of each of its adapters by all of its tokens, with V = 0
+// for the tokens of other adapters, and 0 times an infinity or a NaN in B is a NaN
+// in the output of a token that has nothing to do with that adapter.  A CTA that
+// has seen a sum that is not finite (one FMA an output) comes back to its outputs
+// when all else is done: those that are NaN, and whose feature holds such a value
+// in the B of an adapter that is not the token's, are computed again by the
+// formula, with the token's own adapter alone.  A NaN of the token's own stays as
+// it is.  A warp takes a feature, REDO of its tokens at a time (what the registers of the
+// kernel allow); lane s has slot s of a K' block.
+// Tokens t_lo .. t_hi - 1 of the tile, `rows` rows of this CTA; own: 256 entries of
+// shared memory.  By all threads of the block.
+template <int REDO>
+__device__ __forceinline__ void repair_tile(const FfnArgs &p, bool mid68, int64_t nt, int64_t mt, int rows, int rank,
+                                            int t_lo, int t_hi, int16_t *own) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
+    const int cnt = __ldcg(p.tile_cnt + nt), per = p.r / 8;
+    const int64_t base = __ldcg(p.tile_base + nt), tok0 = nt * p.bn;
+    const int nraw = static_cast<int>(mid68 ? 2 * (p.nkb / 3) : p.nkb), nkb = static_cast<int>(p.nkb);
+    if (cnt == 0) return;
+    __syncthreads();  // the tile before has been read
+    for (int t = t_lo + threadIdx.x; t < t_hi; t += blockDim.x) {
+        // the token's adapter is that of the last request that starts at or before it
+        int32_t lo = 0, hi = p.requests + 1;
+        while (lo < hi) {
+            const int32_t q = lo + (hi - lo) / 2;
+            if (__ldg(p.indptr + q) <= tok0 + t)
+                lo = q + 1;
+            else
+                hi = q;
+        }
+        const int32_t q = lo - 1;
+        const int32_t a = q >= 0 && q < p.requests && tok0 + t < __ldg(p.indptr + q + 1) ? __ldg(p.ids + q) : -1;
+        int slot = -1;
+        for (int s = 0; s < cnt; ++s)
+            if (__ldcg(p.slot_adapter + base + s) == a) slot = s;
+        own[t] = static_cast<int16_t>(slot);
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int rr = warp; rr < rows; rr += nwarps) {
+        const int64_t row = mt * p.tile_rows + (rr >> 7) * 256 + rank * 128 + (rr & 127);
+        if (row >= p.R) continue;
+        int first = cnt, last = -2;  // slots with such a value at this feature; -2: not looked at yet
+#pragma unroll 1
+        for (int t32 = t_lo; t32 < t_hi && last != -1; t32 += 32) {
+            const int t = t32 + lane < t_hi ? t32 + lane : t_lo;
+            const bool nan = t32 + lane < t_hi && (p.Y[(tok0 + t) * p.ldy + row] & 0x7FFFu) > 0x7F80u;
+            if (!__any_sync(0xffffffffu, nan)) continue;
+            if (last == -2) {
+                for (int e = lane; e < cnt * per; e += 32) {
+                    const int s = e / per;
+                    const uint4 b = __ldg(reinterpret_cast<const uint4 *>(
+                        p.B + __ldcg(p.slot_adapter + base + s) * p.sdb + row * p.ldb + (e - s * per) * 8));
+                    bool odd = false;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t w = i == 0 ? b.x : i == 1 ? b.y : i == 2 ? b.z : b.w;
+                        odd |= (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+                    }
+                    if (odd) {
+                        if (s < first) first = s;
+                        if (s > last) last = s;
+                    }
+                }
+                first = __reduce_min_sync(0xffffffffu, first);
+                last = __reduce_max_sync(0xffffffffu, last < 0 ? -1 : last);
+                if (last == -1) break;
+            }
+            uint32_t todo = __ballot_sync(0xffffffffu, nan && (first != own[t] || last != own[t]));
+#pragma unroll 1
+            while (todo != 0) {
+                int tk[REDO], n = 0;  // up to REDO of the tokens; the last one repeated
+#pragma unroll
+                for (int u = 0; u < REDO; ++u) {
+                    tk[u] = todo != 0 ? t32 + __ffs(todo) - 1 : tk[u > 0 ? u - 1 : 0];
+                    n += todo != 0;
+                    todo &= todo - 1;
+                }
+                float sum[REDO] = {};
+                // this lane's slot: its pair of values and the nibble of their two
+                // positions, in the order of packed_geom's blocks (a byte of the metadata
+                // holds two slots of one of 128 rows, in tensor-memory order)
+                const int r7 = rr & 127, pr = lane >> 1;
+                const int byte = ((r7 & 7) + 8 * ((pr >> 1) & 1) + 16 * (r7 >> 4)) * 16 + 4 * (pr >> 2) +
+                                 2 * ((r7 >> 3) & 1) + (pr & 1);
+                const uint32_t *v = reinterpret_cast<const uint32_t *>(p.vals + row * nkb * 64) + lane;
+                const uint8_t *e = p.meta + (row >> 7) * nkb * EBLK_BYTES + byte;
+#pragma unroll 1
+                for (int half = 0; half < (mid68 ? 2 : 1); ++half) {
+                    const uint16_t *src = half ? p.mid : p.src;
+                    const int64_t ld = half ? p.mid_ld : p.src_ld, cols = half ? p.mid_cols : p.src_cols;
+#pragma unroll 2
+                    for (int k = 0; k < (half ? nkb - nraw : nraw); ++k) {
+                        const int64_t kb = !mid68 ? k : (half ? 3 * k + 2 : 3 * (k >> 1) + (k & 1));
+                        const uint32_t pair = __ldg(v + kb * 32);
+                        const uint32_t nib = static_cast<uint32_t>(__ldg(e + kb * EBLK_BYTES)) >> (4 * (lane & 1));
+#pragma unroll
+                        for (int u = 0; u < REDO; ++u) {
+                            const uint2 x = row4(src + (tok0 + tk[u]) * ld, k * 128 + 4 * lane, cols);
+                            const uint32_t x0 = nib & 2u ? x.y : x.x, x1 = nib & 8u ? x.y : x.x;
+                            sum[u] = fmaf(__uint_as_float(pair << 16), __uint_as_float(nib & 1u ? x0 & 0xFFFF0000u : x0 << 16), sum[u]);
+                            sum[u] = fmaf(__uint_as_float(pair & 0xFFFF0000u),
+                                          __uint_as_float(nib & 4u ? x1 & 0xFFFF0000u : x1 << 16), sum[u]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < REDO; ++u) {
+                    const int s = own[tk[u]];
+                    if (s >= 0) {
+                        const uint16_t *b = p.B + __ldcg(p.slot_adapter + base + s) * p.sdb + row * p.ldb;
+                        const uint16_t *vs = p.V + ((base + s) * p.bn + tk[u]) * p.r;
+#pragma unroll 1
+                        for (int j = lane; j < p.r; j += 32)
+                            sum[u] = fmaf(__uint_as_float(static_cast<uint32_t>(__ldcg(vs + j)) << 16),
+                                          __uint_as_float(static_cast<uint32_t>(__ldg(b + j)) << 16), sum[u]);
+                    }
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], d);
+                    if (lane == 0 && u < n) p.Y[(tok0 + tk[u]) * p.ldy + row] = static_cast<uint16_t>(pack_bf16x2(sum[u], 0.0f));
+                }
+            }
+        }
     }
 }
 
@@ -199,6 +347,7 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
     if (warp >= 2 || !p.early) grid_dep_wait();
     // the stream's next kernel may set itself up on SMs that this one leaves
     grid_dep_launch();
+    float odd = 0.0f;  // OP_LORA: NaN once a sum of this thread was not finite
 
     if (warp == 0) {
         // ---------------------------------------------------------- producer
@@ -480,6 +629,9 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
                                 }
                         }
                         if (OP == OP_GLU) gate(f[0], f[NACC - 1], p.act);
+                        if (OP == OP_LORA)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) odd = fmaf(f[0][j], 0.0f, odd);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             if (t + j < nv && rok)
@@ -564,6 +716,9 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
                         }
                         gate(f[0], f[NACC - 1], p.act);
                     }
+                    if (OP == OP_LORA)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) odd = fmaf(f[0][j], 0.0f, odd);
                     emit(p.Y, p.ldy, c, f[0]);
                 }
                 if (c_lo >= c_hi) {
@@ -574,11 +729,22 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
         }
     }
     tc_fence_before();
-    __syncthreads();
+    const bool redo = OP == OP_LORA ? __syncthreads_or(odd != odd) && p.tile_cnt != nullptr : (__syncthreads(), false);
     cluster_sync_all();  // also: no CTA leaves while another reads its sums
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, C::TMEM_COLS);
+    }
+    if (OP == OP_LORA && redo) {
+        grid_dep_wait();
+        for (int64_t tile = cluster; tile < ntiles; tile += nclusters) {
+            int64_t nt, mt;
+            tile_coords(tile, n_t, n_m, band_rows / tile_rows, nt, mt);
+            const int nv = static_cast<int>(T - nt * bn < bn ? T - nt * bn : bn), ng = (nv + 3) / 4;
+            const int t_lo = 4 * (ng * part / split), t_hi = 4 * (ng * (part + 1) / split);  // what this pair stored
+            repair_tile<SPLIT ? 8 : 4>(p, MODE == PMODE_SP68T, nt, mt, second(mt) ? 256 : 128, static_cast<int>(rank), t_lo,
+                        t_hi < nv ? t_hi : nv, reinterpret_cast<int16_t *>(smem));
+        }
     }
 }
 
@@ -1484,6 +1650,23 @@ extern "C" nm_status nm_sparse_gemm_lora(const uint16_t *X, int64_t T, int64_t K
     }
     st = stage_b(X, T, K, ldx, m, g, w, ws, plan.bn, &maps, s);
     if (st != NM_OK) return st;
+    const uint16_t *staged = static_cast<const uint16_t *>(ws);
+    p.src = m == 4 || m == 8 ? X : staged;
+    p.src_ld = m == 4 || m == 8 ? ldx : w.ld;
+    p.src_cols = m == 4 || m == 8 ? K : w.cols;
+    p.mid = staged;
+    p.mid_ld = w.ld;
+    p.mid_cols = w.cols;
+    p.vals = static_cast<const uint16_t *>(packed);
+    p.meta = static_cast<const uint8_t *>(packed) + g.vals_bytes;
+    p.B = B;
+    p.ldb = ldb;
+    p.sdb = sdb;
+    p.V = V;
+    p.r = static_cast<int>(r);
+    p.indptr = indptr;
+    p.ids = ids;
+    p.requests = static_cast<int32_t>(requests);
     if (cap > 0) {
         ShrinkArgs a{};
         a.X = X;
