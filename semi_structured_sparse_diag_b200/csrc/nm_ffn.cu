@@ -49,7 +49,7 @@ struct FfnCfg {
     static constexpr int OFF_A0 = 0, OFF_A1 = A_BYTES, OFF_E0 = 2 * A_BYTES, OFF_E1 = OFF_E0 + EBLK_BYTES;
     static constexpr int OFF_B = OFF_E1 + EBLK_BYTES;  // two atoms of bn/2 tokens x 64 columns
     static constexpr int MAX_STAGES = 6;
-    static constexpr int MAX_SPLIT = 8;         // CTA pairs that share a tile's K' blocks
+    static constexpr int MAX_SPLIT = MAX_PAIRS; // CTA pairs that share a tile's K' blocks
     static constexpr int BAR_BYTES = 256;
     static constexpr int SMEM_BYTES = 232448;
     static constexpr int SMEM_DATA = (SMEM_BYTES - BAR_BYTES - 1024) / 1024 * 1024;
@@ -1287,45 +1287,10 @@ using namespace nm;
 
 namespace {
 
-// clusters of 2 * split blocks of a k_ffn that can be resident at once on
-// the current device (0: none, or a CUDA error), cached per device
-template <auto kernel>
-int64_t ffn_clusters_of(int split) {
-    using Cfg = FfnCfg;
-    static int cache[64][Cfg::MAX_SPLIT + 1] = {};  // count + 1
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (cache[dev][split] == 0) {
-        if (!set_smem_attr<kernel>(Cfg::SMEM_BYTES)) return 0;
-        if (split > 4 && cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
-                             cudaSuccess) {
-            cudaGetLastError();
-            return 0;
-        }
-        cudaLaunchConfig_t q = {};
-        q.gridDim = dim3(static_cast<unsigned>(2 * split * (sm_count() / (2 * split))), 1, 1);
-        q.blockDim = dim3(ffn_threads(split > 1), 1, 1);
-        q.dynamicSmemBytes = Cfg::SMEM_BYTES;
-        cudaLaunchAttribute qa[1];
-        qa[0].id = cudaLaunchAttributeClusterDimension;
-        qa[0].val.clusterDim.x = static_cast<unsigned>(2 * split);
-        qa[0].val.clusterDim.y = 1;
-        qa[0].val.clusterDim.z = 1;
-        q.attrs = qa;
-        q.numAttrs = 1;
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kernel, &q) != cudaSuccess) {
-            cudaGetLastError();
-            n = 0;
-        }
-        cache[dev][split] = n + 1;
-    }
-    return cache[dev][split] - 1;
-}
-
 template <int MODE, int OP>
 int64_t ffn_clusters(int split) {
-    return split > 1 ? ffn_clusters_of<k_ffn<MODE, OP, true>>(split) : ffn_clusters_of<k_ffn<MODE, OP, false>>(1);
+    return split > 1 ? resident_clusters_of<k_ffn<MODE, OP, true>>(split, ffn_threads(true), FfnCfg::SMEM_BYTES)
+                     : resident_clusters_of<k_ffn<MODE, OP, false>>(1, ffn_threads(false), FfnCfg::SMEM_BYTES);
 }
 
 // How a call is cut: tokens per tile and pairs per tile.
@@ -1339,8 +1304,9 @@ struct FfnPlan {
 // 32 clocks and there are four per accumulator and block; the loads come at some
 // 64 bytes a clock) and a fixed part: the epilogue, or with a split the exchange
 // of the sums, 512 bytes per token and accumulator at some 18 bytes a clock.
+// *sure: false if the device could not be asked about some of them.
 template <int MODE, int OP>
-bool ffn_search(int64_t T, int64_t Rpad, int64_t nkb, FfnPlan *best) {
+bool ffn_search(int64_t T, int64_t Rpad, int64_t nkb, FfnPlan *best, bool *sure) {
     using Cfg = FfnCfg;
     const int forced_split = g_sched_policy.load() == 1 ? 1 : 0;
     const int forced_clusters = g_sched_clusters.load();
@@ -1351,6 +1317,7 @@ bool ffn_search(int64_t T, int64_t Rpad, int64_t nkb, FfnPlan *best) {
     for (int split = 1; split <= Cfg::MAX_SPLIT && split <= nkb; ++split) {
         if ((forced_split && split > 1) || (must_split && split == 1)) continue;
         int64_t clusters = ffn_clusters<MODE, OP>(split);
+        if (clusters < 0) *sure = false;
         if (forced_clusters > 0 && forced_clusters < clusters) clusters = forced_clusters;
         if (clusters < 1) continue;
         for (int v = 0; v < (OP == OP_LORA ? 2 : 1) * (bn_top / 16); ++v) {
@@ -1401,10 +1368,14 @@ bool ffn_plan(int64_t T, int64_t Rpad, int64_t nkb, FfnPlan *plan) {
     if (!e.ok || e.T != T || e.Rpad != Rpad || e.nkb != nkb || e.dev != dev || e.policy != policy ||
         e.clusters != clusters) {
         e = Entry{T, Rpad, nkb, dev, policy, clusters, false, {}};
-        e.ok = ffn_search<MODE, OP>(T, Rpad, nkb, &e.plan);
+        bool sure = true;
+        const bool found = ffn_search<MODE, OP>(T, Rpad, nkb, &e.plan, &sure);
+        e.ok = found && sure;
+        *plan = e.plan;
+        return found;
     }
     *plan = e.plan;
-    return e.ok;
+    return true;
 }
 
 template <int MODE, int OP>

@@ -185,6 +185,43 @@ inline uint64_t next_seq() {
     return ctr.fetch_add(1);
 }
 
+// clusters of 2 * pairs blocks of a kernel that can be resident at once on the
+// current device, looked up once per device and number of pairs.  -1: a CUDA call
+// failed; that is not remembered, so that later calls do not depend on it.
+constexpr int MAX_PAIRS = 8;
+template <auto kernel>
+inline int64_t resident_clusters_of(int pairs, int threads, int smem) {
+    static int cache[64][MAX_PAIRS + 1] = {};  // count + 1
+    int dev = 0;
+    if (pairs > MAX_PAIRS || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
+    if (cache[dev][pairs] == 0) {
+        if (!set_smem_attr<kernel>(smem)) return -1;
+        if (pairs > 4 &&
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
+            cudaGetLastError();
+            return -1;
+        }
+        cudaLaunchConfig_t q = {};
+        q.gridDim = dim3(static_cast<unsigned>(2 * pairs * (sm_count() / (2 * pairs))), 1, 1);
+        q.blockDim = dim3(static_cast<unsigned>(threads), 1, 1);
+        q.dynamicSmemBytes = static_cast<size_t>(smem);
+        cudaLaunchAttribute qa[1];
+        qa[0].id = cudaLaunchAttributeClusterDimension;
+        qa[0].val.clusterDim.x = static_cast<unsigned>(2 * pairs);
+        qa[0].val.clusterDim.y = 1;
+        qa[0].val.clusterDim.z = 1;
+        q.attrs = qa;
+        q.numAttrs = 1;
+        int n = 0;
+        if (cudaOccupancyMaxActiveClusters(&n, kernel, &q) != cudaSuccess) {
+            cudaGetLastError();
+            return -1;
+        }
+        cache[dev][pairs] = n + 1;
+    }
+    return cache[dev][pairs] - 1;
+}
+
 // extra device memory the online phase needs for (2N-2):2N patterns: the
 // gathered middle windows (6:8) or the lifted activations (4:6, 8:10)
 struct GemmWs {

@@ -121,7 +121,7 @@ struct GradCfg {
     static constexpr int A_BYTES = 128 * 128, B_BYTES = 128 * 128;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int STAGES = 6;
-    static constexpr int MAX_SPLIT = 8;
+    static constexpr int MAX_SPLIT = MAX_PAIRS;
     static constexpr int SUM_BYTES = 256 * 128 * 4;        // a CTA's sums, over the idle stages
     static constexpr int EPI_WARPS = 8;
     static constexpr int EPI_BYTES = EPI_WARPS * 32 * 128;  // 32 rows x 64 columns bf16 each
@@ -542,40 +542,9 @@ size_t grad_bytes(int64_t T, int64_t R) {  // one of dG, dU
     return (static_cast<size_t>(T) * static_cast<size_t>(padded8(R)) * 2 + 255) / 256 * 256;
 }
 
-// clusters of 2 * split blocks that can be resident at once on the current
-// device (0: none, or a CUDA error), cached per device
-template <auto kernel>
+template <bool SPLIT>
 int64_t grad_clusters(int split) {
-    using Cfg = GradCfg;
-    static int cache[64][Cfg::MAX_SPLIT + 1] = {};  // count + 1
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
-    if (cache[dev][split] == 0) {
-        if (!set_smem_attr<kernel>(Cfg::SMEM_BYTES)) return 0;
-        if (split > 4 &&
-            cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess) {
-            cudaGetLastError();
-            return 0;
-        }
-        cudaLaunchConfig_t q = {};
-        q.gridDim = dim3(static_cast<unsigned>(2 * split * (sm_count() / (2 * split))), 1, 1);
-        q.blockDim = dim3(Cfg::THREADS, 1, 1);
-        q.dynamicSmemBytes = Cfg::SMEM_BYTES;
-        cudaLaunchAttribute qa[1];
-        qa[0].id = cudaLaunchAttributeClusterDimension;
-        qa[0].val.clusterDim.x = static_cast<unsigned>(2 * split);
-        qa[0].val.clusterDim.y = 1;
-        qa[0].val.clusterDim.z = 1;
-        q.attrs = qa;
-        q.numAttrs = 1;
-        int n = 0;
-        if (cudaOccupancyMaxActiveClusters(&n, kernel, &q) != cudaSuccess) {
-            cudaGetLastError();
-            n = 0;
-        }
-        cache[dev][split] = n + 1;
-    }
-    return cache[dev][split] - 1;
+    return resident_clusters_of<k_gemm_grad<SPLIT>>(split, GradCfg::THREADS, GradCfg::SMEM_BYTES);
 }
 
 nm_status launch_grad(const GradMaps &maps, GradArgs p, cudaStream_t s) {
@@ -587,13 +556,13 @@ nm_status launch_grad(const GradMaps &maps, GradArgs p, cudaStream_t s) {
     const int policy = g_sched_policy.load(), bound = g_sched_clusters.load();
     auto bounded = [&](int64_t n) { return bound > 0 && bound < n ? static_cast<int64_t>(bound) : n; };
     int split = 1;
-    int64_t clusters = bounded(grad_clusters<k_gemm_grad<false>>(1));
+    int64_t clusters = bounded(grad_clusters<false>(1));
     const int64_t blocks = 2 * ((p.R + 63) / 64);
     int64_t best = policy == 2 ? INT64_MAX : blocks * 600;
     for (int i = 2; i <= Cfg::MAX_SPLIT && p.tiles_x > 0 && i <= blocks && policy != 1; ++i) {
         const int64_t cost = (blocks + i - 1) / i * 600 + 10000;
         if (cost >= best) continue;
-        const int64_t n = bounded(grad_clusters<k_gemm_grad<true>>(i));
+        const int64_t n = bounded(grad_clusters<true>(i));
         if (n < p.tiles_x) continue;
         best = cost;
         split = i;
