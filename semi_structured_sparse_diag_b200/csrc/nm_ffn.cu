@@ -36,7 +36,6 @@
 namespace nm {
 
 enum { OP_GLU = 0, OP_LORA = 1 };
-enum { ACT_SILU = 0, ACT_GELU = 1, ACT_RELU2 = 2 };
 
 // epilogue warps: what a tile waits for is their latency, so the plain kernel has
 // sixteen; the exchange of a split needs more registers than that leaves
@@ -100,23 +99,23 @@ struct FfnArgs {
 // 1 / (1 + e^-2z); e^x overflowing to inf gives 0; max(g, 0)^2 keeps a NaN
 template <int ACT>
 __device__ __forceinline__ float act_fn(float g) {
-    if (ACT == ACT_RELU2) return g < 0.0f ? 0.0f : g * g;
-    const float z = ACT == ACT_SILU ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g);
+    if (ACT == NM_ACT_RELU2) return g < 0.0f ? 0.0f : g * g;
+    const float z = ACT == NM_ACT_SILU ? g : 1.5957691216057308f * (g + 0.044715f * g * g * g);
     return __fdividef(g, 1.0f + __expf(-z));
 }
 
 // g[i] = act(g[i]) u[i]
 template <int N>
 __device__ __forceinline__ void gate(float (&g)[N], const float (&u)[N], int act) {
-    if (act == ACT_SILU) {
+    if (act == NM_ACT_SILU) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) g[i] = act_fn<ACT_SILU>(g[i]) * u[i];
-    } else if (act == ACT_GELU) {
+        for (int i = 0; i < N; ++i) g[i] = act_fn<NM_ACT_SILU>(g[i]) * u[i];
+    } else if (act == NM_ACT_GELU) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) g[i] = act_fn<ACT_GELU>(g[i]) * u[i];
+        for (int i = 0; i < N; ++i) g[i] = act_fn<NM_ACT_GELU>(g[i]) * u[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) g[i] = act_fn<ACT_RELU2>(g[i]) * u[i];
+        for (int i = 0; i < N; ++i) g[i] = act_fn<NM_ACT_RELU2>(g[i]) * u[i];
     }
 }
 
@@ -1514,7 +1513,7 @@ extern "C" nm_status nm_sparse_glu(const uint16_t *X, int64_t T, int64_t K, int6
     if (!X || !packed_gate || !packed_up || !H || (G == nullptr) != (U == nullptr)) return NM_ERR_NULL;
     nm_status st = check_ffn_sizes(T, K, R, m);
     if (st != NM_OK) return st;
-    if (act < ACT_SILU || act > ACT_RELU2) return NM_ERR_UNSUPPORTED;
+    if (act < NM_ACT_SILU || act > NM_ACT_RELU2) return NM_ERR_UNSUPPORTED;
     if (ldx < K || ldh < R || (G && ldgu < R)) return NM_ERR_SHAPE;
     if (!aligned16(X) || !aligned16(packed_gate) || !aligned16(packed_up) || !aligned16(H) || (ldx % 8) != 0 ||
         (ldh % 8) != 0 || (G && (!aligned16(G) || !aligned16(U) || (ldgu % 8) != 0)) || (ws && !aligned16(ws)))

@@ -1719,10 +1719,6 @@ __global__ void __launch_bounds__(256)
 // ===========================================================================
 using namespace nm;
 
-namespace {
-
-}  // namespace
-
 nm_status nm::launch_gather_mid(const uint16_t *X, int64_t T, int64_t K, int64_t ldx, int64_t G,
                                 uint16_t *Xmid, int64_t ldm, cudaStream_t s) {
     const int64_t pairs = (G + 1) / 2;
@@ -1733,9 +1729,6 @@ nm_status nm::launch_gather_mid(const uint16_t *X, int64_t T, int64_t K, int64_t
 }
 
 namespace {
-
-// one flag per kernel instantiation and device (kernels of different modes
-// share a signature, so the cache is keyed on the kernel itself)
 
 // ---- single-CTA kernel (ablation baseline)
 constexpr int GEMM_BN = 128;

@@ -19,19 +19,17 @@
 
 namespace nm {
 
-enum { GACT_SILU = 0, GACT_GELU = 1, GACT_RELU2 = 2 };
-
 // act(g) and act'(g) in fp32.  silu: s = 1/(1+e^-g), s(1 + g(1-s)).  gelu (tanh
 // form), with z = c(g + a g^3): s = 1/(1+e^-2z) = (1 + tanh z)/2, slope
 // s + 2 g s (1-s) c (1 + 3 a g^2).  relu^2: 2 max(g, 0).
 __device__ __forceinline__ void act_and_slope(float g, int act, float &f, float &d) {
-    if (act == GACT_RELU2) {
+    if (act == NM_ACT_RELU2) {
         const float r = g < 0.0f ? 0.0f : g;
         f = r * r;
         d = 2.0f * r;
         return;
     }
-    if (act == GACT_SILU) {
+    if (act == NM_ACT_SILU) {
         const float e = __expf(-g), s = __fdividef(1.0f, 1.0f + e);
         f = g * s;
         d = s * (1.0f + g * (1.0f - s));
@@ -612,7 +610,7 @@ extern "C" nm_status nm_sparse_glu_backward(const uint16_t *dH, int64_t lddh, co
     if (T < 1 || K < 1 || R < 1 || T > 0x7FFFFFFF - 512 || K > 0x7FFFFFFF - 512 || R > 0x7FFFFFFF - 512 ||
         lddh < R || ldgu < R || (need_w && (ldx < K || lddw < K)) || (dX && (ldw < K || lddx < K)))
         return NM_ERR_SHAPE;
-    if (act < GACT_SILU || act > GACT_RELU2 || (mask_gate && (m < 2 || m > 16))) return NM_ERR_UNSUPPORTED;
+    if (act < NM_ACT_SILU || act > NM_ACT_RELU2 || (mask_gate && (m < 2 || m > 16))) return NM_ERR_UNSUPPORTED;
     if (!aligned16(dH) || !aligned16(G) || !aligned16(U) || !aligned16(ws) || (lddh % 8) != 0 || (ldgu % 8) != 0 ||
         (dX && (!aligned16(Wg) || !aligned16(Wu) || !aligned16(dX) || (ldw % 8) != 0 || (lddx % 8) != 0)) ||
         (need_w && (!aligned16(X) || !aligned16(dWg) || !aligned16(dWu) || (ldx % 8) != 0 || (lddw % 8) != 0)) ||
