@@ -489,6 +489,8 @@ def _scratch(ws, need, X):
         if need == 0:
             return None, 0, None
         ws = _out(need, dtype=torch.uint8, device=X.device)
+    elif not ws.is_contiguous():  # its bytes are not the ones behind its first
+        raise NMError("ws must be contiguous")
     return ws.data_ptr(), ws.numel() * ws.element_size(), ws
 
 
