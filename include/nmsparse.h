@@ -472,7 +472,11 @@ nm_status nm_sparse_densify(const uint16_t *vals, const uint32_t *mask, int64_t 
  *       nm_sparse_gemm): V, then the product, scheduled as nm_sparse_glu's with
  *       tiles of 256 or 512 rows.  V costs one pass over X per adapter of a tile
  *       of up to 240 tokens, the product one dense block of 64 ranks (four
- *       adapters of rank <= 16, two of rank <= 32) per tile.
+ *       adapters of rank <= 16, two of rank <= 32) per tile.  V is kept as a
+ *       [tokens of a tile x r] block per adapter of the tile, zero in the rows of
+ *       other tokens: with about as many adapters as tokens it and its traffic
+ *       grow with tokens x the tile's width (8192 requests of one token, 240
+ *       adapters: 252 MB of workspace at rank 64, 1.0 GB at rank 256).
  *   ws : nm_sparse_gemm_lora_workspace_bytes(...) bytes, 16-byte aligned,
  *       required.  Not to be shared by calls that may run at the same time.  A
  *       captured call may be replayed (with other contents of every array), and

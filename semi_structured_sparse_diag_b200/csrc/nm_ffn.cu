@@ -24,7 +24,7 @@
 // 713 us in a long run, which the power cap bounds (1.4 GHz); 494 us at
 // 1965 MHz, the tensor pipe 68% active: 15 us of products and 5 us of epilogue a
 // tile, the latter bound by all SMs' stores at once.  8192 tokens with rank 64
-// adapters 355 to 380 us, of which the product 284 and V 41.
+// adapters 330 to 380 us, of which the product 284 and V 41.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -95,7 +95,9 @@ struct FfnArgs {
     int r;
 };
 
-// silu g / (1 + e^-g); gelu (tanh form) g / (1 + e^-2z), since (1 + tanh z) / 2 =
+// __expf and __fdividef: good to 2^-21 (1 + |x|) and 2 units, far below the rounding
+// to bf16 that follows (the quotient of a divisor above 2^126, |g| > 87, is 0 for
+// 1e-36).  silu g / (1 + e^-g); gelu (tanh form) g / (1 + e^-2z), since (1 + tanh z) / 2 =
 // 1 / (1 + e^-2z); e^x overflowing to inf gives 0; max(g, 0)^2 keeps a NaN
 template <int ACT>
 __device__ __forceinline__ float act_fn(float g) {

@@ -94,9 +94,11 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------------------
-// The three products, in one launch unless they are large: dense bf16 operands, fp32 accumulation,
-// bf16 results.  Persistent CTA pairs, 256 x 256 tiles, two accumulators in
-// tensor memory (the epilogue of a tile overlaps the next tile's MMAs), six
+// The three products, in one launch unless they are large: dense bf16 operands,
+// fp32 accumulation, bf16 results.  8192 tokens, 11008 x 4096, in a loop of seconds
+// at the power cap: 93% of cuBLAS' rate for the same products (dX some 1.14 ms to 1.05,
+// dWg and dWu 1.17 to 1.09; 1.2 GHz against 1.4 to 1.5).
+// Persistent CTA pairs, 256 x 256 tiles, two accumulators in tensor memory (the epilogue of a tile overlaps the next tile's MMAs), six
 // 32 KB stages; warps as in k_gemm_pair, with the loading and the issuing warp
 // in step and one lane of each at work.
 //   dX  [T x K]: A = dG, then dU [T x R] (K-major), B = Wg, then Wu [R x K]
@@ -478,6 +480,9 @@ __global__ void __launch_bounds__(GradCfg::THREADS, 1)
 // per mask word (32 columns).  Every group holds n kept values, so a word's
 // first value sits at (groups before it) n + the kept positions of the group
 // that the word's start cuts.  grid: x over words, y (+65535 z) over rows.
+// 11008 x 4096: 2:4 52 us, 6:8 51, floors 22 and 25 (141 and 163 MB); bound by a
+// two-byte load per kept value.  It runs once a training step beside products of
+// milliseconds.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(128)
     k_densify(const uint16_t *__restrict__ vals, const uint32_t *__restrict__ mask, int64_t R, int64_t K, int n,
