@@ -136,12 +136,14 @@ __device__ __forceinline__ uint2 row4(const uint16_t *__restrict__ row, int64_t 
 
 // A tile multiplies the B of each of its adapters by all of its tokens, with V = 0
 // for the tokens of other adapters, and 0 times an infinity or a NaN in B is a NaN
-// in the output of a token that has nothing to do with that adapter.  A CTA that
-// has seen a sum that is not finite (one FMA an output) comes back to its outputs
-// when all else is done: those that are NaN, and whose feature holds such a value
-// in the B of an adapter that is not the token's, are computed again by the
-// formula, with the token's own adapter alone.  A NaN of the token's own stays as
-// it is.  A warp takes a feature, REDO of its tokens at a time (what the registers of the
+// in the output of a token that has nothing to do with that adapter.  Then no
+// output of that feature is finite for any token of the tile, so a thread of the
+// epilogue that has seen that of all of its tokens (one bitwise AND an output; a
+// few NaN tokens, as behind the last request, do not look like it) sends its CTA
+// back to its outputs when all else is done: those that are NaN, and whose feature
+// holds such a value in the B of an adapter that is not the token's, are computed
+// again by the formula, with the token's own adapter alone.  A NaN of the token's
+// own stays as it is.  A warp takes a feature, REDO of its tokens at a time (what the registers of the
 // kernel allow); lane s has slot s of a K' block.
 // Tokens t_lo .. t_hi - 1 of the tile, `rows` rows of this CTA; own: 256 entries of
 // shared memory.  By all threads of the block.
@@ -180,7 +182,9 @@ __device__ __forceinline__ void repair_tile(const FfnArgs &p, bool mid68, int64_
 #pragma unroll 1
         for (int t32 = t_lo; t32 < t_hi && last != -1; t32 += 32) {
             const int t = t32 + lane < t_hi ? t32 + lane : t_lo;
-            const bool nan = t32 + lane < t_hi && (p.Y[(tok0 + t) * p.ldy + row] & 0x7FFFu) > 0x7F80u;
+            const uint32_t y = t32 + lane < t_hi ? p.Y[(tok0 + t) * p.ldy + row] & 0x7FFFu : 0x7F80u;
+            const bool nan = y > 0x7F80u;
+            if (__any_sync(0xffffffffu, y < 0x7F80u)) break;  // a finite output: no such B at this feature
             if (!__any_sync(0xffffffffu, nan)) continue;
             if (last == -2) {
                 for (int e = lane; e < cnt * per; e += 32) {
@@ -348,7 +352,9 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
     if (warp >= 2 || !p.early) grid_dep_wait();
     // the stream's next kernel may set itself up on SMs that this one leaves
     grid_dep_launch();
-    float odd = 0.0f;  // OP_LORA: NaN once a sum of this thread was not finite
+    // OP_LORA: a feature of this thread had no finite sum for any of its tokens
+    constexpr uint32_t EXPONENT = 0x7F800000u;
+    bool odd = false;
 
     if (warp == 0) {
         // ---------------------------------------------------------- producer
@@ -578,6 +584,7 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
                 // this pair's share of the tokens, four at a time; all the parts of
                 // GROUPS x 4 tokens are in flight before the first is used
                 constexpr int GROUPS = OP == OP_GLU ? 1 : 2;
+                uint32_t all = ~0u;  // AND of the sums' bits
                 const int ng = (nv + 3) / 4, g1 = active ? ng * (part + 1) / split : 0;
                 const int gstep = ntp;
                 const uint32_t off = smem_u32(mine);
@@ -632,7 +639,7 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
                         if (OP == OP_GLU) gate(f[0], f[NACC - 1], p.act);
                         if (OP == OP_LORA)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) odd = fmaf(f[0][j], 0.0f, odd);
+                            for (int j = 0; j < 4; ++j) all &= __float_as_uint(f[0][j]);
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
                             if (t + j < nv && rok)
@@ -641,6 +648,7 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
                 }
                 __syncwarp();
                 if (lane < split) mbar_arrive_cluster(mapa_shared(sum_free, 2 * lane + rank));
+                odd |= ng * part / split + tp < g1 && (all & EXPONENT) == EXPONENT;
             }
             if constexpr (!SPLIT) {
                 // 32 rows x 16 tokens at a time, as 8 x 8 blocks: out of tensor memory in
@@ -691,6 +699,7 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
                         }
                     }
                 };
+                uint32_t all[4] = {~0u, ~0u, ~0u, ~0u};  // ANDs of the bits of this thread's four rows
 #pragma unroll 1
                 for (int c = c_lo; c < c_hi; ++c) {
                     uint32_t v[NACC][2][8];
@@ -719,9 +728,12 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
                     }
                     if (OP == OP_LORA)
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) odd = fmaf(f[0][j], 0.0f, odd);
+                        for (int j = 0; j < 16; ++j) all[2 * (j >> 3) + ((j >> 1) & 1)] &= __float_as_uint(f[0][j]);
                     emit(p.Y, p.ldy, c, f[0]);
                 }
+                if (OP == OP_LORA)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) odd |= c_lo < c_hi && (all[i] & EXPONENT) == EXPONENT;
                 if (c_lo >= c_hi) {
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster(acc_empty_cl);
@@ -730,7 +742,7 @@ __global__ void __launch_bounds__(ffn_threads(SPLIT), 1)
         }
     }
     tc_fence_before();
-    const bool redo = OP == OP_LORA ? __syncthreads_or(odd != odd) && p.tile_cnt != nullptr : (__syncthreads(), false);
+    const bool redo = OP == OP_LORA ? __syncthreads_or(odd) && p.tile_cnt != nullptr : (__syncthreads(), false);
     cluster_sync_all();  // also: no CTA leaves while another reads its sums
     if (warp == 1) {
         tc_fence_after();

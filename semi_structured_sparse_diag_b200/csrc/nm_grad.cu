@@ -95,12 +95,12 @@ __global__ void __launch_bounds__(256)
 
 // ---------------------------------------------------------------------------
 // The three products, in one launch unless they are large: dense bf16 operands,
-// fp32 accumulation, bf16 results.  8192 tokens, 11008 x 4096, in a loop of seconds
-// at the power cap: 93% of cuBLAS' rate for the same products (dX some 1.14 ms to 1.05,
-// dWg and dWu 1.17 to 1.09; 1.2 GHz against 1.4 to 1.5).
-// Persistent CTA pairs, 256 x 256 tiles, two accumulators in tensor memory (the epilogue of a tile overlaps the next tile's MMAs), six
-// 32 KB stages; warps as in k_gemm_pair, with the loading and the issuing warp
-// in step and one lane of each at work.
+// fp32 accumulation, bf16 results.  Persistent CTA pairs, 256 x 256 tiles, two
+// accumulators in tensor memory (the epilogue of a tile overlaps the next tile's
+// MMAs), six 32 KB stages; warps as in k_gemm_pair, with the loading and the issuing
+// warp in step and one lane of each at work.  8192 tokens, 11008 x 4096, in a loop
+// of seconds at the power cap: 93% of cuBLAS' rate for the same products (dX some
+// 1.14 ms to 1.05, dWg and dWu 1.17 to 1.09; 1.2 GHz against 1.4 to 1.5).
 //   dX  [T x K]: A = dG, then dU [T x R] (K-major), B = Wg, then Wu [R x K]
 //       (MN-major); the contraction is R twice.
 //   dWg, dWu [R x K]: A = dG or dU [T x R], B = X [T x K], both MN-major,
