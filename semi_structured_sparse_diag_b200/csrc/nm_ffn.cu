@@ -821,9 +821,7 @@ struct ShrinkArgs {
 };
 
 struct TilePlan {
-    // per token of the tile: the request that starts there, its end << 32 | its adapter
-    // + 2; 0: none
-    unsigned long long start[256];
+    int32_t start[256];            // per token of the tile: the request that starts there, -1: none
     int32_t slot[256];             // the token's slot, -1: none
     int32_t adapter[256];          // of a slot
     int32_t keys[SHRINK_HASH], first[SHRINK_HASH];
@@ -837,13 +835,13 @@ struct TilePlan {
 // beyond the slots there are is left out).  The blocks of a cluster each make the
 // plan of their tile and meet at as many barriers as it has slots and tokens, so it
 // depends on the list alone: of requests that a wrong list starts on one token the
-// one that ends last counts (its adapter the highest), not the last to be written.
+// last in the list counts, not the last to be written.
 __device__ bool plan_tile(const ShrinkArgs &p, int64_t tile, TilePlan &plan) {
     constexpr int NT = SHRINK_THREADS;
     const int i = threadIdx.x, warp = i >> 5, lane = i & 31;
     const int64_t t0 = tile * p.bn, t1 = t0 + p.bn;
     bool bad = false;
-    for (int k = i; k < 256; k += NT) plan.start[k] = 0ull;
+    for (int k = i; k < 256; k += NT) plan.start[k] = -1;
     for (int k = i; k < SHRINK_HASH; k += NT) {
         plan.keys[k] = -1;
         plan.first[k] = 256;
@@ -858,7 +856,7 @@ __device__ bool plan_tile(const ShrinkArgs &p, int64_t tile, TilePlan &plan) {
         before += hi <= t0;
         if (!odd && lo < hi && hi > t0 && lo < t1) {
             const int at = lo > t0 ? static_cast<int>(lo - t0) : 0;
-            atomicMax(&plan.start[at], static_cast<unsigned long long>(hi) << 32 | (static_cast<uint32_t>(a) + 2u));
+            atomicMax(&plan.start[at], q);
         }
     }
     if (before) atomicAdd(&plan.before, before);
@@ -867,7 +865,7 @@ __device__ bool plan_tile(const ShrinkArgs &p, int64_t tile, TilePlan &plan) {
     int mine[2], a[2], h[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
-        int m = plan.start[i + u * NT] != 0ull ? i + u * NT : -1;
+        int m = plan.start[i + u * NT] >= 0 ? i + u * NT : -1;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, m, d);
@@ -885,8 +883,8 @@ __device__ bool plan_tile(const ShrinkArgs &p, int64_t tile, TilePlan &plan) {
         a[u] = -1;
         h[u] = 0;
         if (tok < p.bn && mine[u] >= 0) {
-            const unsigned long long st = plan.start[mine[u]];
-            if (t0 + tok < static_cast<int64_t>(st >> 32)) a[u] = static_cast<int>(static_cast<uint32_t>(st) - 2u);
+            const int32_t q = plan.start[mine[u]];
+            if (t0 + tok < __ldg(p.indptr + q + 1)) a[u] = __ldg(p.ids + q);
         }
         if (a[u] >= 0) {
             h[u] = static_cast<int>((static_cast<uint32_t>(a[u]) * 2654435761u) >> 23);
