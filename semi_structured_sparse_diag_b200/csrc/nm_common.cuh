@@ -431,16 +431,31 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t *bar, uint32_t parity
     }
 }
 
-// The same waits for a warp that stays in step: every lane waits, and all of them
-// get the same answer.  A wait's limit is each lane's own clock, so near it some
-// lanes may see the barrier and others give up; a loop that went on or ended lane
-// by lane would leave half of a warp at the next warp-wide instruction for good.
-__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+// The same waits for a warp that stays in step: all lanes poll, and each poll and
+// the end of the limit is one answer of the warp.  (By its own clock a lane near
+// the limit may see the barrier where another gives up; a loop that went on or
+// ended lane by lane would leave half of a warp at the next warp-wide instruction
+// for good.)  Device time of a projection with one token's adapter: 14.1 us; with a
+// vote after each lane's own wait 14.6, with one lane that polls 16.5.
+template <bool CLUSTER>
+__device__ __forceinline__ bool wait_in_step(uint64_t *bar, uint32_t parity) {
+    auto complete = [&] {
+        return __all_sync(0xffffffffu, CLUSTER ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) != 0;
+    };
+    if (complete()) return true;
+    const uint64_t t0 = global_timer_ns(), limit = wait_limit_ns();
+    uint32_t spins = 0;
+    while (true) {
+        if (complete()) return true;
+        if ((++spins & 255u) == 0 && __any_sync(0xffffffffu, global_timer_ns() - t0 > limit)) {
+            raise_error(ERRBIT_TIMEOUT);
+            return false;
+        }
+    }
 }
-
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t *bar, uint32_t parity) { return wait_in_step<false>(bar, parity); }
 __device__ __forceinline__ bool mbar_wait_cluster_warp(uint64_t *bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity));
+    return wait_in_step<true>(bar, parity);
 }
 
 // TMA tile load of a CTA pair: data lands in this CTA's shared memory, the

@@ -26,10 +26,14 @@ def test_warps_in_step_wait_together(name):
 
 
 def test_a_common_wait_is_a_vote():
+    # every poll and the end of the limit: no lane returns by itself
     text = source("nm_common.cuh")
-    for name in ("mbar_wait", "mbar_wait_cluster"):
-        body = re.search(rf"bool {name}_warp\([^)]*\) {{(.*?)}}", text, re.S).group(1)
-        assert re.fullmatch(rf"\s*return __all_sync\(0xffffffffu, {name}\(bar, parity\)\);\s*", body)
+    body = re.search(r"bool wait_in_step\([^)]*\) {(.*?)\n}", text, re.S).group(1)
+    assert re.search(r"auto complete = \[&\] {\s*return __all_sync\(0xffffffffu, [^;]*\) != 0;\s*};", body)
+    assert re.findall(r"if \((.*)\) (?:return true;|{)", body) == [
+        "complete()", "complete()", "(++spins & 255u) == 0 && __any_sync(0xffffffffu, global_timer_ns() - t0 > limit)"]
+    for name in ("mbar_wait_warp", "mbar_wait_cluster_warp"):
+        assert re.search(rf"bool {name}\(uint64_t \*bar, uint32_t parity\) {{\s*return wait_in_step<(true|false)>\(bar, parity\);\s*}}", text)
 
 
 def test_stream_k_flags_are_taken_by_the_warp():
